@@ -72,7 +72,8 @@ typedef enum gsa_status {
   GSA_ERR_TIMEOUT = 5      /* reported by gsa_workspace_status: a bounded device wait expired */
 } gsa_status;
 
-typedef enum gsa_dtype { GSA_F32 = 0, GSA_BF16 = 1 } gsa_dtype;
+/* GSA_I8 and GSA_E4M3: codes of a paged raw-token cache only (gsa_pdesc). */
+typedef enum gsa_dtype { GSA_F32 = 0, GSA_BF16 = 1, GSA_I8 = 2, GSA_E4M3 = 3 } gsa_dtype;
 
 /* Which partial softmax result a producer left in ws for gsa_unfold_attend. */
 typedef enum gsa_prior {
@@ -89,11 +90,12 @@ typedef enum gsa_op {
   GSA_OP_PREFILL = 2,
   GSA_OP_HGSA2 = 3,
   GSA_OP_GIST_STEP = 4,
-  GSA_OP_MULTIQUERY = 5
+  GSA_OP_MULTIQUERY = 5,
+  GSA_OP_PAGED = 6 /* every gsa_paged_* call, and the decode steps between them */
 } gsa_op;
 
 /* Device-side status bits (gsa_workspace_status). */
-#define GSA_DEVERR_BAD_INDEX 0x1u /* a sel_idx entry >= N was skipped */
+#define GSA_DEVERR_BAD_INDEX 0x1u /* a sel_idx entry >= N, or a page outside the pool, was skipped */
 #define GSA_DEVERR_TIMEOUT 0x2u   /* an mbarrier wait exceeded its iteration bound */
 #define GSA_DEVERR_CAPACITY 0x4u  /* a count exceeded a capacity and was clamped */
 
@@ -125,6 +127,26 @@ typedef struct gsa_h2desc {
   gsa_hdesc level1;
   gsa_hdesc level2;
 } gsa_h2desc;
+
+/* A paged raw-token cache.  Raw row r of sequence b lies in page
+ * page_table[b][r / page] at row r % page of it. */
+typedef struct gsa_pdesc {
+  int32_t cache_dtype; /* GSA_I8 or GSA_E4M3; gsa_paged_append also desc->dtype (no scales) */
+  int32_t page;        /* rows per page: a multiple of desc->chunk */
+  int32_t n_pages;     /* pages of the pool; n_pages * page * hkv < 2^32 */
+  int32_t max_pages;   /* page-table entries per sequence; max_pages * page >= t_max */
+} gsa_pdesc;
+
+/* What gsa_paged_append appends. */
+typedef struct gsa_append_desc {
+  int32_t n_tok;       /* tokens of all sequences together, >= 0 */
+  int32_t rot_dim;     /* leading dims of a head that the position turns: 0 (none) or a multiple of 16, <= d */
+  int32_t interleaved; /* pairs of rotated dims: 0: (i, i + rot_dim/2); 1: (2i, 2i + 1) */
+  int32_t advance;     /* 1: own_len[b] grows by the tokens that joined; 0: own_len is left as it is */
+  /* elements from one token's row to the next of q_new / k_new / v_new (a
+   * fused projection's rows); 0: packed.  A multiple of 16 bytes. */
+  int32_t q_stride, k_stride, v_stride;
+} gsa_append_desc;
 
 /* Human-readable name of a status code (static string). */
 const char *gsa_status_string(int32_t status);
@@ -426,6 +448,84 @@ gsa_status gsa_prefill_attend(const gsa_desc *desc, const void *q_raw, const voi
 gsa_status gsa_prefill(const gsa_desc *desc, const void *q_raw, const void *k_raw, const void *v_raw,
                        const void *q_gist, const void *k_gist, const void *v_gist, int32_t *sel_idx,
                        float *sel_score, void *out_raw, void *out_gist, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Paged raw-token cache held in 8 bits ------------------------------
+ * A deployment variant: the pages describe no cache format.  The raw rows of
+ * all sequences share a pool of pages,
+ *   k_pages, v_pages [n_pages, hkv, page, d] in cache_dtype,
+ *   k_scale, v_scale [n_pages, hkv, page / chunk] fp32 (8-bit types),
+ * and a row's value is scale * code, with one scale for each chunk (block) of
+ * rows and kv head: s = max|x| / 127 (GSA_I8) or the least power of two with
+ * max|x| / s <= 448 (GSA_E4M3).  Scales are 0 (a block of zeros: max|x| below
+ * 2^-100), between 2^-110 and 2^126, or NaN (a block that received an inf or
+ * NaN; every row of it reads as NaN).
+ *   page_table [batch, max_pages] int32; entries past a sequence's rows are
+ *   not read.  A row whose page lies outside the pool is left out and flagged
+ *   (GSA_DEVERR_BAD_INDEX).  Sequences may share pages that are only read.
+ * Rows of sequence b: n_gists[b] * chunk + own_len[b], or own_len[b] where
+ * n_gists may be NULL and is (a cache without gists: any length), clamped to
+ * t_max.  Gists stay in their own unpaged arrays.  batch <= 8192.  One
+ * workspace of gsa_workspace_bytes(desc, GSA_OP_PAGED, NULL) bytes serves all
+ * of these calls and the score / select calls between them. */
+
+/* New tokens join the cache behind the rows it holds.
+ *   q_new [n_tok, hq, d] or NULL, k_new, v_new [n_tok, hkv, d] in desc->dtype
+ *   cu_tok [batch + 1] int32: tokens cu_tok[b] .. cu_tok[b+1]-1 belong to
+ *          sequence b (ascending; token rows outside every sequence are
+ *          ignored); NULL: n_tok / batch tokens each
+ *   pos    [n_tok] int32 positions, or NULL: the raw row
+ *   inv_freq [rot_dim / 2] fp32: pair i turns by pos * inv_freq[i] (the angle
+ *          is reduced in 64 bits)
+ *   q_out  [n_tok, hq, d] in desc->dtype: the turned queries (not q_new's
+ *          buffer).  Keys are stored turned, values as they are.
+ * A block that a call part-fills takes more rows in a later call: its scale
+ * can only grow, and the codes it holds are then rounded once more to the new
+ * scale.  The first row of a block starts it anew, whatever its scale was.
+ * Rows past t_max are dropped, their queries with them, and flagged
+ * (GSA_DEVERR_CAPACITY).  No page may
+ * be written for two sequences in one call.  With cache_dtype = desc->dtype,
+ * page = t_max, n_pages = batch and page_table[b] = b the pool is the raw_k /
+ * raw_v layout of the unpaged calls. */
+gsa_status gsa_paged_append(const gsa_desc *desc, const gsa_pdesc *pdesc, const gsa_append_desc *adesc,
+                            const void *q_new, const void *k_new, const void *v_new, const int32_t *cu_tok,
+                            const int32_t *pos, const float *inv_freq, const int32_t *page_table,
+                            const int32_t *n_gists, int32_t *own_len, void *k_pages, void *v_pages, float *k_scale,
+                            float *v_scale, void *q_out, void *ws, size_t ws_bytes, void *stream);
+
+/* Dense attention over every raw row of each sequence (the layers that keep
+ * full attention; the baseline of the sparse step).  n_q query tokens per
+ * sequence (1..64), the last n_q of its rows: query i sees the first
+ * rows - (n_q - 1) + i of them.
+ *   q [batch, n_q, hq, d], out [batch, n_q, hq, d] in out_dtype,
+ *   lse [batch, n_q, hq] fp32 or NULL.  No visible row: out 0, lse -inf.
+ * topk and exclude_unselected are ignored. */
+gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_t n_q, const void *q,
+                            const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                            const int32_t *page_table, const int32_t *n_gists, const int32_t *own_len, void *out,
+                            float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* gsa_unfold_attend with the raw rows in the paged cache; every other
+ * argument, the prior and the workspace as there. */
+gsa_status gsa_paged_unfold(const gsa_desc *desc, const gsa_pdesc *pdesc, const void *q, const void *k_pages,
+                            const void *v_pages, const float *k_scale, const float *v_scale,
+                            const int32_t *page_table, const void *gist_v, const int32_t *n_gists,
+                            const int32_t *own_len, const int32_t *sel_idx, const float *sel_score, int32_t prior,
+                            void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* gsa_decode with the raw rows in the paged cache. */
+gsa_status gsa_paged_decode(const gsa_desc *desc, const gsa_pdesc *pdesc, const void *q, const void *gist_k,
+                            const void *gist_v, const void *k_pages, const void *v_pages, const float *k_scale,
+                            const float *v_scale, const int32_t *page_table, const int32_t *n_gists,
+                            const int32_t *own_len, void *out, float *lse, int32_t *sel_idx, float *sel_score,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/* gsa_gist_step with the raw rows in the paged cache.  Workspace:
+ * gsa_workspace_bytes(desc, GSA_OP_PAGED, NULL). */
+gsa_status gsa_paged_gist_step(const gsa_desc *desc, const gsa_pdesc *pdesc, const void *q, const void *k_new,
+                               const void *v_new, void *gist_k, void *gist_v, const void *k_pages,
+                               const void *v_pages, const float *k_scale, const float *v_scale,
+                               const int32_t *page_table, int32_t *n_gists, int32_t *own_len, void *out, float *lse,
+                               void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,9 +17,10 @@ import torch
 from .build import LIB
 
 GSA_OK, GSA_ERR_INVALID_ARG, GSA_ERR_UNSUPPORTED, GSA_ERR_WORKSPACE, GSA_ERR_CUDA, GSA_ERR_TIMEOUT = range(6)
-GSA_F32, GSA_BF16 = 0, 1
+GSA_F32, GSA_BF16, GSA_I8, GSA_E4M3 = 0, 1, 2, 3
 GSA_PRIOR_NONE, GSA_PRIOR_GISTS, GSA_PRIOR_HGSA, GSA_PRIOR_HGSA2 = 0, 1, 2, 3
 GSA_OP_DECODE, GSA_OP_HGSA, GSA_OP_PREFILL, GSA_OP_HGSA2, GSA_OP_GIST_STEP, GSA_OP_MULTIQUERY = 0, 1, 2, 3, 4, 5
+GSA_OP_PAGED = 6
 GSA_DEVERR_BAD_INDEX, GSA_DEVERR_TIMEOUT, GSA_DEVERR_CAPACITY = 1, 2, 4
 
 EXPORTS = (
@@ -27,6 +28,7 @@ EXPORTS = (
     "gsa_score_gists", "gsa_topk_select", "gsa_topp_select", "gsa_unfold_attend", "gsa_decode", "hgsa_select",
     "hgsa_decode", "hgsa2_select", "hgsa2_decode", "gsa_decode_backward", "gsa_gist_step", "gsa_multiquery_select", "gsa_prefill_score", "gsa_prefill_attend", "gsa_prefill",
     "gsa_decode_noalloc", "gsa_noalloc_status", "gsa_score_select",
+    "gsa_paged_append", "gsa_paged_attend", "gsa_paged_unfold", "gsa_paged_decode", "gsa_paged_gist_step",
 )
 
 
@@ -51,6 +53,15 @@ class gsa_h2desc(C.Structure):
     _fields_ = [("level1", gsa_hdesc), ("level2", gsa_hdesc)]
 
 
+class gsa_pdesc(C.Structure):
+    _fields_ = [("cache_dtype", C.c_int32), ("page", C.c_int32), ("n_pages", C.c_int32), ("max_pages", C.c_int32)]
+
+
+class gsa_append_desc(C.Structure):
+    _fields_ = [("n_tok", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("advance", C.c_int32),
+                ("q_stride", C.c_int32), ("k_stride", C.c_int32), ("v_stride", C.c_int32)]
+
+
 _lib = None
 
 
@@ -65,7 +76,7 @@ def load(path: Path | None = None) -> C.CDLL:
                            "(the GSA kernels have no CPU fallback)")
     lib = C.CDLL(str(p))
     vp, sz, i32 = C.c_void_p, C.c_size_t, C.c_int32
-    D, H = C.POINTER(gsa_desc), C.POINTER(gsa_hdesc)
+    D, H, P = C.POINTER(gsa_desc), C.POINTER(gsa_hdesc), C.POINTER(gsa_pdesc)
     sig = {
         "gsa_status_string": ([i32], C.c_char_p),
         "gsa_version": ([], i32),
@@ -90,6 +101,11 @@ def load(path: Path | None = None) -> C.CDLL:
         "gsa_decode_noalloc": ([D, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
         "gsa_noalloc_status": ([vp, C.POINTER(C.c_uint32)], i32),
         "gsa_score_select": ([D] + [vp] * 8 + [sz, vp], i32),
+        "gsa_paged_append": ([D, P, C.POINTER(gsa_append_desc)] + [vp] * 15 + [sz, vp], i32),
+        "gsa_paged_attend": ([D, P, i32] + [vp] * 11 + [sz, vp], i32),
+        "gsa_paged_unfold": ([D, P] + [vp] * 11 + [i32] + [vp] * 3 + [sz, vp], i32),
+        "gsa_paged_decode": ([D, P] + [vp] * 15 + [sz, vp], i32),
+        "gsa_paged_gist_step": ([D, P] + [vp] * 15 + [sz, vp], i32),
     }
     for name, (argt, rest) in sig.items():
         fn = getattr(lib, name)
@@ -112,6 +128,15 @@ def make_desc(batch, hq, hkv, d, chunk, n_max, t_max, topk, exclude_unselected=F
 
 def make_hdesc(group, topk_meta, m_max) -> gsa_hdesc:
     return gsa_hdesc(group, topk_meta, m_max)
+
+
+def make_pdesc(cache_dtype, page, n_pages, max_pages) -> gsa_pdesc:
+    return gsa_pdesc(cache_dtype, page, n_pages, max_pages)
+
+
+def make_append_desc(n_tok, rot_dim=0, interleaved=False, advance=False, q_stride=0, k_stride=0,
+                     v_stride=0) -> gsa_append_desc:
+    return gsa_append_desc(n_tok, rot_dim, int(bool(interleaved)), int(bool(advance)), q_stride, k_stride, v_stride)
 
 
 def make_h2desc(level1: gsa_hdesc, level2: gsa_hdesc) -> gsa_h2desc:
@@ -441,3 +466,125 @@ def gsa_noalloc_status(stream=None) -> int:
     if st not in (GSA_OK, GSA_ERR_TIMEOUT):
         _check("gsa_noalloc_status", st)
     return int(flags.value)
+
+
+# ------------------------------------------------- paged raw-token cache
+_CACHE_DT = {GSA_F32: torch.float32, GSA_BF16: torch.bfloat16, GSA_I8: torch.int8, GSA_E4M3: torch.float8_e4m3fn}
+
+
+def _here(*tensors):
+    """CUDA tensors lie on the current device (their pointers are used on its stream)."""
+    dev = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if dev is None:
+                dev = torch.cuda.current_device()
+            if t.device.index != dev:
+                raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(t, dtype, name, n_tok, heads, d, stride):
+    """Data pointer of token rows [n_tok, heads, d], `stride` elements apart (0: packed)."""
+    want = (stride or heads * d, d, 1)
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 3 or t.shape[0] < n_tok or tuple(t.shape[1:]) != (heads, d):
+        raise ValueError(f"{name} must be [>= {n_tok}, {heads}, {d}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the GSA path has no CPU implementation)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if n_tok and (t.stride()[2] != 1 or (heads > 1 and t.stride()[1] != d) or (n_tok > 1 and t.stride()[0] != want[0])):
+        raise ValueError(f"{name} has strides {t.stride()}, the descriptor says {want}")
+    return C.c_void_p(t.data_ptr())
+
+
+def _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table):
+    """The pool's pointer arguments, in the order of the C calls."""
+    dt = _CACHE_DT.get(pdesc.cache_dtype)
+    coded = pdesc.cache_dtype in (GSA_I8, GSA_E4M3)
+    pool = pdesc.n_pages * pdesc.page * desc.hkv
+    ns = pool // desc.chunk if desc.chunk > 0 else 0
+    nt = desc.batch * pdesc.max_pages
+    _here(k_pages, v_pages, k_scale, v_scale, page_table)
+    return (_ptr(k_pages, dt, "k_pages", numel=pool * desc.d), _ptr(v_pages, dt, "v_pages", numel=pool * desc.d),
+            _ptr(k_scale, torch.float32, "k_scale", not coded, ns),
+            _ptr(v_scale, torch.float32, "v_scale", not coded, ns), _ptr(page_table, torch.int32, "page_table", numel=nt))
+
+
+def gsa_paged_append(desc, pdesc, adesc, q_new, k_new, v_new, cu_tok, pos, inv_freq, page_table, n_gists, own_len,
+                     k_pages, v_pages, k_scale, v_scale, q_out, ws, stream=None):
+    dt, n, i32 = _TORCH_DT[desc.dtype], adesc.n_tok, torch.int32
+    _here(q_new, k_new, v_new, cu_tok, pos, inv_freq, n_gists, own_len, q_out, ws)
+    kp, vp_, ks, vs, table = _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table)
+    q = q_o = None
+    if q_new is not None:
+        q = _rows(q_new, dt, "q_new", n, desc.hq, desc.d, adesc.q_stride)
+        q_o = _ptr(q_out, dt, "q_out", numel=n * desc.hq * desc.d)
+    _check("gsa_paged_append", load().gsa_paged_append(
+        C.byref(desc), C.byref(pdesc), C.byref(adesc), q,
+        _rows(k_new, dt, "k_new", n, desc.hkv, desc.d, adesc.k_stride),
+        _rows(v_new, dt, "v_new", n, desc.hkv, desc.d, adesc.v_stride),
+        _ptr(cu_tok, i32, "cu_tok", True, desc.batch + 1), _ptr(pos, i32, "pos", True, n),
+        _ptr(inv_freq, torch.float32, "inv_freq", adesc.rot_dim == 0, adesc.rot_dim // 2),
+        table, _ptr(n_gists, i32, "n_gists", True, desc.batch), _ptr(own_len, i32, "own_len", numel=desc.batch),
+        kp, vp_, ks, vs, q_o, *_ws(ws), _stream(stream)))
+
+
+def gsa_paged_attend(desc, pdesc, n_q, q, k_pages, v_pages, k_scale, v_scale, page_table, n_gists, own_len, out, lse,
+                     ws, stream=None):
+    _here(q, n_gists, own_len, out, lse, ws)
+    nq = max(int(n_q), 0)
+    _check("gsa_paged_attend", load().gsa_paged_attend(
+        C.byref(desc), C.byref(pdesc), int(n_q), _ptr(q, _TORCH_DT[desc.dtype], "q", numel=nq * _n(desc, "q")),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
+        _ptr(n_gists, torch.int32, "n_gists", True, desc.batch),
+        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
+        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=nq * _n(desc, "q")),
+        _ptr(lse, torch.float32, "lse", True, nq * _n(desc, "heads")), *_ws(ws), _stream(stream)))
+
+
+def gsa_paged_unfold(desc, pdesc, q, k_pages, v_pages, k_scale, v_scale, page_table, gist_v, n_gists, own_len, sel_idx,
+                     sel_score, prior, out, lse, ws, stream=None):
+    dt = _TORCH_DT[desc.dtype]
+    _here(q, gist_v, n_gists, own_len, sel_idx, sel_score, out, lse, ws)
+    _check("gsa_paged_unfold", load().gsa_paged_unfold(
+        C.byref(desc), C.byref(pdesc), _ptr(q, dt, "q", numel=_n(desc, "q")),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
+        _ptr(gist_v, dt, "gist_v", True, _n(desc, "gists")), _ptr(n_gists, torch.int32, "n_gists", numel=desc.batch),
+        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
+        _ptr(sel_idx, torch.int32, "sel_idx", True, _n(desc, "sel")),
+        _ptr(sel_score, torch.float32, "sel_score", True, _n(desc, "sel")), int(prior),
+        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=_n(desc, "q")),
+        _ptr(lse, torch.float32, "lse", True, _n(desc, "heads")), *_ws(ws), _stream(stream)))
+
+
+def gsa_paged_decode(desc, pdesc, q, gist_k, gist_v, k_pages, v_pages, k_scale, v_scale, page_table, n_gists, own_len,
+                     out, lse=None, sel_idx=None, sel_score=None, ws=None, stream=None):
+    dt = _TORCH_DT[desc.dtype]
+    _here(q, gist_k, gist_v, n_gists, own_len, out, lse, sel_idx, sel_score, ws)
+    _check("gsa_paged_decode", load().gsa_paged_decode(
+        C.byref(desc), C.byref(pdesc), _ptr(q, dt, "q", numel=_n(desc, "q")),
+        _ptr(gist_k, dt, "gist_k", numel=_n(desc, "gists")), _ptr(gist_v, dt, "gist_v", numel=_n(desc, "gists")),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
+        _ptr(n_gists, torch.int32, "n_gists", numel=desc.batch),
+        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
+        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=_n(desc, "q")),
+        _ptr(lse, torch.float32, "lse", True, _n(desc, "heads")),
+        _ptr(sel_idx, torch.int32, "sel_idx", True, _n(desc, "sel")),
+        _ptr(sel_score, torch.float32, "sel_score", True, _n(desc, "sel")), *_ws(ws), _stream(stream)))
+
+
+def gsa_paged_gist_step(desc, pdesc, q, k_new, v_new, gist_k, gist_v, k_pages, v_pages, k_scale, v_scale, page_table,
+                        n_gists, own_len, out, lse, ws, stream=None):
+    dt = _TORCH_DT[desc.dtype]
+    _here(q, k_new, v_new, gist_k, gist_v, n_gists, own_len, out, lse, ws)
+    _check("gsa_paged_gist_step", load().gsa_paged_gist_step(
+        C.byref(desc), C.byref(pdesc), _ptr(q, dt, "q", numel=_n(desc, "q")),
+        _ptr(k_new, dt, "k_new", numel=_n(desc, "kv_new")), _ptr(v_new, dt, "v_new", numel=_n(desc, "kv_new")),
+        _ptr(gist_k, dt, "gist_k", numel=_n(desc, "gists")), _ptr(gist_v, dt, "gist_v", numel=_n(desc, "gists")),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
+        _ptr(n_gists, torch.int32, "n_gists", numel=desc.batch),
+        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
+        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=_n(desc, "q")),
+        _ptr(lse, torch.float32, "lse", True, _n(desc, "heads")), *_ws(ws), _stream(stream)))

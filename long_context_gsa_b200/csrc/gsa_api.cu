@@ -13,9 +13,11 @@
 
 #include "../../include/gsa.h"
 #include "common.cuh"
+#include "k_append.cuh"
 #include "k_backward.cuh"
 #include "k_gist_step.cuh"
 #include "k_hgsa.cuh"
+#include "k_paged.cuh"
 #include "k_prefill.cuh"
 #include "k_score.cuh"
 #include "k_select.cuh"
@@ -31,6 +33,8 @@ constexpr int kUnfoldSplitMax = 32;  // partial slots per row from the unfold pa
 constexpr int kHgsaSplitMax = 32;    // partial slots per row from the H-GSA pass
 constexpr int kTopkSmemCap = 16384;  // keys kept in shared memory by the top-k kernel
 constexpr int kMaxTopk = kTopkMax;
+constexpr int kPgMaxQueries = 64;                     // query tokens per sequence of the paged attention
+constexpr int kPgMaxGroups = kPgMaxQueries * 16 / 8;  // its segments of 8 query rows per kv head
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -46,6 +50,7 @@ struct Layout {
   size_t meta2_scores = 0, meta2_idx = 0, cand1_scores = 0, cand1_ids = 0, cand1_count = 0;
   size_t pf_stats = 0, pf_gist = 0, pf_vh = 0, pf_ovf = 0;
   size_t gs_cur = 0, gs_plus = 0;
+  size_t pg_append = 0, pg_seg = 0, pg_part = 0;
   size_t total = 0;
 };
 
@@ -145,6 +150,13 @@ Layout layout(const gsa_desc *d, int32_t op, const gsa_hdesc *h) {
   }
   if (op == GSA_OP_GIST_STEP) {
     take(L.gs_cur, static_cast<size_t>(d->batch) * 4);
+    take(L.gs_plus, static_cast<size_t>(d->batch) * 4);
+  }
+  if (op == GSA_OP_PAGED) {
+    take(L.pg_append, 256);
+    take(L.pg_seg, static_cast<size_t>(d->batch) * d->hkv * kPgMaxGroups * 4);
+    take(L.pg_part, static_cast<size_t>(kPgMaxCtas) * 2 * kPgMaxRows * rec);
+    take(L.gs_cur, static_cast<size_t>(d->batch) * 4);  // gsa_paged_gist_step runs in this workspace too
     take(L.gs_plus, static_cast<size_t>(d->batch) * 4);
   }
   if (op == GSA_OP_HGSA2 && h) {  // h points at a gsa_h2desc: level1, then level2
@@ -816,6 +828,35 @@ gsa_desc gist_step_desc(const gsa_desc *d) {
   return g;
 }
 
+// What comes before the raw rows in a gist-position step: the new gist joins
+// the gist arrays, and the scoring pass leaves the partial of gists 0..N.
+gsa_status gist_step_front(const gsa_desc *g, const void *q, const void *k_new, const void *v_new, void *gist_k,
+                           void *gist_v, const int32_t *n_gists, const Layout &L, void *ws, int *n_prior,
+                           void *stream) {
+  uint32_t *status = reinterpret_cast<uint32_t *>(at(ws, L.status));
+  int32_t *n_cur = reinterpret_cast<int32_t *>(at(ws, L.gs_cur));
+  int32_t *n_plus = reinterpret_cast<int32_t *>(at(ws, L.gs_plus));
+  GistAppendArgs ga;
+  ga.k_new = static_cast<const uint4 *>(k_new);
+  ga.v_new = static_cast<const uint4 *>(v_new);
+  ga.gist_k = static_cast<uint4 *>(gist_k);
+  ga.gist_v = static_cast<uint4 *>(gist_v);
+  ga.n_gists = n_gists;
+  ga.n_cur = n_cur;
+  ga.n_plus = n_plus;
+  ga.hkv = g->hkv;
+  ga.n_max = g->n_max;
+  ga.row_vecs = static_cast<int32_t>(static_cast<size_t>(g->d) * elem_size(g->dtype) / 16);
+  ga.status = status;
+  // 1. the new gist joins the gist arrays at row N (counted as N+1 by the scoring pass)
+  GSA_TRY(launch(k_gist_append, dim3(g->hkv, g->batch), dim3(32), 0, stream, ga));
+  // 2. the compression-mask attention: gists 0..N through the scoring pass's
+  //    partial, chunk N's raw rows through the unfold (no selected chunk)
+  float *scores = reinterpret_cast<float *>(at(ws, L.scores));
+  float *part = reinterpret_cast<float *>(at(ws, L.part_g));
+  return run_score(g, q, gist_k, gist_v, n_plus, 1, g->n_max, scores, g->n_max, part, n_prior, status, stream);
+}
+
 // Each (batch, kv head) pair is split into the same number of CTAs, chosen
 // so the launch is about kBwdWaves full waves of resident CTAs.
 template <int D, typename T, int GM>
@@ -844,12 +885,12 @@ const char *gsa_status_string(int32_t s) {
   }
 }
 
-int32_t gsa_version(void) { return 100; }
+int32_t gsa_version(void) { return 200; }
 
 size_t gsa_workspace_bytes(const gsa_desc *desc, int32_t op, const gsa_hdesc *hdesc) {
   if (check_desc(desc) != GSA_OK) return 0;
   if (op != GSA_OP_DECODE && op != GSA_OP_HGSA && op != GSA_OP_PREFILL && op != GSA_OP_HGSA2 &&
-      op != GSA_OP_GIST_STEP && op != GSA_OP_MULTIQUERY)
+      op != GSA_OP_GIST_STEP && op != GSA_OP_MULTIQUERY && op != GSA_OP_PAGED)
     return 0;
   if (op == GSA_OP_MULTIQUERY && check_multiquery(desc) != GSA_OK) return 0;
   if (op == GSA_OP_GIST_STEP) {
@@ -1197,37 +1238,19 @@ gsa_status gsa_gist_step(const gsa_desc *desc, const void *q, const void *k_new,
   const gsa_desc g = gist_step_desc(desc);
   const Layout L = layout(&g, GSA_OP_GIST_STEP, nullptr);
   if (ws_bytes < L.total) return GSA_ERR_WORKSPACE;
-  uint32_t *status = reinterpret_cast<uint32_t *>(at(ws, L.status));
-  int32_t *n_cur = reinterpret_cast<int32_t *>(at(ws, L.gs_cur));
-  int32_t *n_plus = reinterpret_cast<int32_t *>(at(ws, L.gs_plus));
-  GistAppendArgs ga;
-  ga.k_new = static_cast<const uint4 *>(k_new);
-  ga.v_new = static_cast<const uint4 *>(v_new);
-  ga.gist_k = static_cast<uint4 *>(gist_k);
-  ga.gist_v = static_cast<uint4 *>(gist_v);
-  ga.n_gists = n_gists;
-  ga.n_cur = n_cur;
-  ga.n_plus = n_plus;
-  ga.hkv = g.hkv;
-  ga.n_max = g.n_max;
-  ga.row_vecs = static_cast<int32_t>(static_cast<size_t>(g.d) * elem_size(g.dtype) / 16);
-  ga.status = status;
-  // 1. the new gist joins the gist arrays at row N (counted as N+1 by the scoring pass)
-  GSA_TRY(launch(k_gist_append, dim3(g.hkv, g.batch), dim3(32), 0, stream, ga));
-  // 2. the compression-mask attention: gists 0..N through the scoring pass's
-  //    partial, chunk N's raw rows through the unfold (no selected chunk)
-  float *scores = reinterpret_cast<float *>(at(ws, L.scores));
-  float *part = reinterpret_cast<float *>(at(ws, L.part_g));
+  const int32_t *n_cur = reinterpret_cast<int32_t *>(at(ws, L.gs_cur));
+  const int32_t *n_plus = reinterpret_cast<int32_t *>(at(ws, L.gs_plus));
   int n_prior = 0;
-  GSA_TRY(run_score(&g, q, gist_k, gist_v, n_plus, 1, g.n_max, scores, g.n_max, part, &n_prior, status, stream));
+  GSA_TRY(gist_step_front(&g, q, k_new, v_new, gist_k, gist_v, n_gists, L, ws, &n_prior, stream));
+  const float *part = reinterpret_cast<float *>(at(ws, L.part_g));
   if (cudaMemsetAsync(at(ws, L.counters), 0, static_cast<size_t>(g.batch) * g.hq * 4,
                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return GSA_ERR_CUDA;
   GSA_TRY(run_unfold(&g, q, raw_k, raw_v, gist_v, n_cur, own_len, reinterpret_cast<int32_t *>(at(ws, L.sel_idx)),
                      reinterpret_cast<float *>(at(ws, L.sel_score)), part, n_prior, out, lse, L, ws, stream));
   // 3. chunk completion: n_gists = N+1, own_len = 0
-  return launch(k_gist_commit, dim3(cdiv(g.batch, 128)), dim3(128), 0, stream, static_cast<const int32_t *>(n_cur),
-                static_cast<const int32_t *>(n_plus), n_gists, own_len, static_cast<int>(g.batch));
+  return launch(k_gist_commit, dim3(cdiv(g.batch, 128)), dim3(128), 0, stream, n_cur, n_plus, n_gists, own_len,
+                static_cast<int>(g.batch));
 }
 
 gsa_status hgsa2_select(const gsa_desc *desc, const gsa_h2desc *h2desc, const void *q, const void *meta2_k,
@@ -1441,3 +1464,5 @@ extern "C" gsa_status gsa_noalloc_status(void *stream, uint32_t *flags_out) {
   // reading it needs no allocation, only a copy into the caller's variable.
   return gsa_workspace_status(ws, GSA_NOALLOC_SCRATCH_BYTES, stream, flags_out);
 }
+
+#include "paged_api.cuh"

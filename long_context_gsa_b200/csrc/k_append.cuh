@@ -1,0 +1,342 @@
+// k_append.cuh -- new keys and values join a paged raw-token cache, with the
+// position rotation applied on the way and 8-bit blocks quantised.
+//
+// A pair (x, y) of a head's rotated dims at position p and frequency w turns
+// by the angle p w: (x cos - y sin, y cos + x sin).  The angle is reduced in
+// 64 bits (p w / 2 pi loses whole turns in fp32 once p w passes about 10^5),
+// the sine and cosine and the products are fp32.
+//
+// 8-bit caches: a block of `chunk` rows of one kv head has one fp32 scale s,
+// codes round(x / s).  int8: s = max|x| / 127.  e4m3: s is the least power
+// of two with max|x| / s <= 448, so x / s is exact, and moving codes to a
+// larger scale loses only what falls into e4m3's subnormals.  A block whose
+// max|x| is below 2^-100 has scale 0 and codes 0; one that receives an inf or
+// NaN has scale NaN.  Rows that join a part-filled block can only raise its
+// scale; the rows already held are then re-expressed (rounded once more).
+//
+// What bounds it: HBM (each new row read and written once) for long inputs,
+// launch and three dependent loads for single tokens.  A CTA takes one block
+// of one sequence for all heads (or a share of the heads when there are few
+// blocks), so the sines of a row are computed once and every block of codes
+// has one writer; a warp takes one (block, head) at a time, 8 dims a lane.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "k_paged.cuh"
+
+namespace gsa {
+
+enum { kFmtPlain = 2 };
+
+struct AppendArgs {
+  const void *q, *k, *v;       // [n_tok, heads, D], rows q_stride / k_stride / v_stride elements apart; q may be null
+  const int32_t *cu;           // [B + 1] or null (n_tok / B tokens each)
+  const int32_t *pos;          // [n_tok] or null (the raw row)
+  const float *inv_freq;       // [rot / 2]
+  const int32_t *table;        // [B, max_pages]
+  const int32_t *n_gists;      // or null
+  int32_t *own_len;            // read; advanced by the last CTA when `advance`
+  void *kp, *vp;               // pages
+  float *ks, *vs;              // scales (8-bit)
+  void *q_out;                 // [n_tok, hq, D]
+  int64_t q_stride, k_stride, v_stride;
+  int32_t n_tok, B, hq, hkv, n_max, t_max, n_pages, max_pages, blocks;
+  int32_t rot, inter, advance;
+  FastDiv page, chunk;
+  uint32_t *counter, *status;
+};
+
+constexpr int kApThreads = 256;
+constexpr int kApWarps = kApThreads / 32;
+
+// First new raw row and number of new rows of sequence b, cut at t_max.
+__device__ __forceinline__ int append_span(const AppendArgs &a, int b, int &start, int &tok0) {
+  int64_t s = max(__ldcg(a.own_len + b), 0);
+  if (a.n_gists) s += static_cast<int64_t>(min(max(__ldcg(a.n_gists + b), 0), a.n_max)) * a.chunk.d;
+  int n;
+  if (a.cu) {
+    tok0 = min(max(__ldcg(a.cu + b), 0), a.n_tok);
+    n = min(max(__ldcg(a.cu + b + 1), 0), a.n_tok) - tok0;
+  } else {
+    n = a.n_tok / a.B;
+    tok0 = b * n;
+  }
+  n = max(n, 0);
+  start = static_cast<int>(s < a.t_max ? s : a.t_max);
+  if (start + static_cast<int64_t>(n) > a.t_max) {
+    flag_error(a.status, GSA_DEVERR_CAPACITY);
+    n = a.t_max - start;
+  }
+  return n;
+}
+
+// Eight elements of T at p as floats.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float *x) {
+  if (sizeof(T) == 2) {
+    Vec16<__nv_bfloat16>::unpack(ldg_nc_v4(p), x);
+  } else {
+    Vec16<float>::unpack(ldg_nc_v4(p), x);
+    Vec16<float>::unpack(ldg_nc_v4(reinterpret_cast<const float *>(p) + 4), x + 4);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float *x) {
+  if (sizeof(T) == 2) {
+    uint4 w;
+    uint32_t *u = &w.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = w;
+  } else {
+    float4 *f = reinterpret_cast<float4 *>(p);
+    f[0] = make_float4(x[0], x[1], x[2], x[3]);
+    f[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// Dims e .. e + 7 of the row at p, turned by the row's table of (cos, sin).
+// Halves: dim i pairs with i + rot / 2; interleaved: 2 i with 2 i + 1.  rot
+// is a multiple of 16, so the 8 dims lie in one half, and so do their
+// partners.
+template <typename T>
+__device__ __forceinline__ void load_turned(const T *p, int e, int rot, int inter, const float2 *cs, float *x) {
+  load8(p + e, x);
+  if (e >= rot) return;
+  if (inter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 c = cs[e / 2 + i];
+      const float u = x[2 * i], v = x[2 * i + 1];
+      x[2 * i] = fmaf(u, c.x, -(v * c.y));
+      x[2 * i + 1] = fmaf(v, c.x, u * c.y);
+    }
+  } else {
+    const int half = rot >> 1;
+    const bool up = e >= half;
+    const int f = up ? e - half : e;
+    float y[8];
+    load8(p + (up ? f : e + half), y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 c = cs[f + i];
+      x[i] = fmaf(x[i], c.x, up ? y[i] * c.y : -(y[i] * c.y));
+    }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);  // an inf or NaN among the values
+  if (amax_bits < static_cast<uint32_t>(127 - 100) << 23) return 0.f;  // below 2^-100
+  if (FMT == kFmtI8) return __fdiv_rn(__uint_as_float(amax_bits), 127.f);
+  // amax = f 2^e, 1 <= f < 2; 448 = 1.75 * 2^8
+  const int e = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
+// Eight codes of x * inv.
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const float *x, float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float *y = x + 4 * h;
+    if (FMT == kFmtI8) {
+      uint32_t u = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = min(max(__float2int_rn(y[i] * inv), -127), 127);
+        u |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
+      }
+      w[h] = u;
+    } else {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE, __NV_E4M3);
+      w[h] = lo | (hi << 16);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 c, float *x) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t lo, hi;
+    codes_to_h2<FMT>(w[h], lo, hi);
+    const float2 a = unpack_h2(lo), b = unpack_h2(hi);
+    x[4 * h] = a.x;
+    x[4 * h + 1] = a.y;
+    x[4 * h + 2] = b.x;
+    x[4 * h + 3] = b.y;
+  }
+}
+
+// One (block, kv head) of keys (TURN) or values: n new rows from token row
+// `src` on (stride elements apart) go to page row `dst`.., `held` rows of the
+// block come before them.
+template <int D, typename T, int FMT, bool TURN>
+__device__ __forceinline__ void append_block(const T *src, int64_t stride, int n, int held, void *pages, size_t dst,
+                                             float *scale, int rot, int inter, const float2 *cs) {
+  constexpr int L = D / 8, RPW = 32 / L;  // lanes of a row, rows of a pass
+  const int lane = threadIdx.x & 31, sub = lane / L, e = 8 * (lane % L);
+  float x[8];
+  auto load = [&](int r) {
+    if (TURN)
+      load_turned(src + r * stride, e, rot, inter, cs + r * (rot / 2), x);
+    else
+      load8(src + r * stride + e, x);
+  };
+  if (FMT == kFmtPlain) {
+    T *out = static_cast<T *>(pages) + dst * D;
+#pragma unroll 2
+    for (int r = sub; r < n; r += RPW) {
+      load(r);
+      store8(out + static_cast<size_t>(r) * D + e, x);
+    }
+    return;
+  }
+  constexpr int F = FMT == kFmtPlain ? kFmtI8 : FMT;  // (the plain case has returned)
+  uint32_t amax = 0;
+#pragma unroll 2
+  for (int r = sub; r < n; r += RPW) {
+    load(r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  const float old = held > 0 ? __ldcg(scale) : 0.f;
+  float s = block_scale<F>(amax);
+  if (!(s > old) && s == s) s = old;  // the larger; NaN from either stays
+  uint8_t *out = static_cast<uint8_t *>(pages) + dst * D;
+  if (s > old && held > 0) {
+    const float ratio = old / s;
+    uint8_t *first = out - static_cast<size_t>(held) * D;
+    for (int r = sub; r < held; r += RPW) {
+      uint2 *p = reinterpret_cast<uint2 *>(first + static_cast<size_t>(r) * D + e);
+      float y[8];
+      decode8<F>(__ldcg(p), y);
+      *p = encode8<F>(y, ratio);
+    }
+  }
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;  // 0 for a scale of 0 or NaN: codes 0
+#pragma unroll 2
+  for (int r = sub; r < n; r += RPW) {
+    load(r);
+    uint2 c = make_uint2(0, 0);
+    if (inv > 0.f) c = encode8<F>(x, inv);
+    *reinterpret_cast<uint2 *>(out + static_cast<size_t>(r) * D + e) = c;
+  }
+  __syncwarp();
+  if (lane == 0) *scale = s;
+}
+
+// Grid (x, y): CTA x takes blocks x, x + gridDim.x, .. of the line of all
+// sequences' touched blocks; the y CTAs share a block's heads.
+template <int D, typename T, int FMT>
+__global__ void __launch_bounds__(kApThreads, 4) k_paged_append(const AppendArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  float2 *cs = reinterpret_cast<float2 *>(smem);  // [chunk][rot / 2]
+  uint32_t *pre = reinterpret_cast<uint32_t *>(cs + a.chunk.d * (a.rot / 2));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunk = a.chunk.d, half = a.rot >> 1;
+  pdl_wait();
+  paged_prefix<kApThreads>(pre, a.B, [&](int b) {
+    int start, tok0;
+    const int n = append_span(a, b, start, tok0);
+    return n > 0 ? a.chunk.div(start + n - 1) - a.chunk.div(start) + 1 : 0u;
+  });
+  const uint32_t total = pre[a.B];
+  constexpr int L = D / 8, RPW = 32 / L;
+  for (uint32_t u = blockIdx.x; u < total; u += gridDim.x) {
+    const int b = paged_find(pre, a.B, u);
+    int start, tok0;
+    const int n = append_span(a, b, start, tok0);
+    const int blk = a.chunk.div(start) + (u - pre[b]);
+    const int r0 = max(start, blk * chunk), r1 = min(start + n, (blk + 1) * chunk);  // t_max <= 2^28
+    const int rows = r1 - r0, held = r0 - blk * chunk;
+    const int64_t tok = tok0 + (r0 - start);
+    const uint32_t pg = a.page.div(r0);
+    const int pid = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + pg);
+    const bool live = static_cast<uint32_t>(pid) < static_cast<uint32_t>(a.n_pages);
+    if (!live && tid == 0) flag_error(a.status, GSA_DEVERR_BAD_INDEX);
+    const int off = r0 - static_cast<int>(pg) * static_cast<int>(a.page.d);
+    for (int i = tid; i < rows * half; i += kApThreads) {
+      const int r = i / half, f = i - r * half;
+      const int p = a.pos ? __ldcg(a.pos + tok + r) : r0 + r;
+      // turns in 64 bits; the fraction of a turn as fp32 plus its remainder
+      const double turns = static_cast<double>(p) * static_cast<double>(__ldcg(a.inv_freq + f)) * 0.15915494309189535;
+      const double fr = 2.0 * (turns - rint(turns));
+      const float hi = static_cast<float>(fr);
+      const float lo = static_cast<float>(fr - static_cast<double>(hi)) * 3.14159265f;
+      float sn, cn;
+      sincospif(hi, &sn, &cn);
+      cs[i] = make_float2(fmaf(-lo, sn, cn), fmaf(lo, cn, sn));
+    }
+    __syncthreads();
+    // tasks: K and V of each kv head, then the queries' rows in passes of RPW
+    const int kv_tasks = live ? 2 * a.hkv : 0;
+    const int q_rows = a.q ? rows * a.hq : 0;
+    const int tasks = kv_tasks + (q_rows + 2 * RPW - 1) / (2 * RPW);
+    for (int i = blockIdx.y * kApWarps + warp; i < tasks; i += gridDim.y * kApWarps) {
+      if (i < kv_tasks) {
+        const bool is_v = i >= a.hkv;
+        const int h = is_v ? i - a.hkv : i;
+        const size_t ph = static_cast<size_t>(pid) * a.hkv + h;
+        const size_t dst = ph * a.page.d + off, si = ph * a.blocks + a.chunk.div(off);
+        if (is_v)
+          append_block<D, T, FMT, false>(static_cast<const T *>(a.v) + tok * a.v_stride + static_cast<size_t>(h) * D,
+                                         a.v_stride, rows, held, a.vp, dst, a.vs + si, 0, 0, nullptr);
+        else
+          append_block<D, T, FMT, true>(static_cast<const T *>(a.k) + tok * a.k_stride + static_cast<size_t>(h) * D,
+                                        a.k_stride, rows, held, a.kp, dst, a.ks + si, a.rot, a.inter, cs);
+      } else {
+        const int e = 8 * (lane % L);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int j = ((i - kv_tasks) * 2 + x) * RPW + lane / L;
+          if (j < q_rows) {
+            const int r = j / a.hq, h = j - r * a.hq;
+            float y[8];
+            load_turned(static_cast<const T *>(a.q) + (tok + r) * a.q_stride + static_cast<size_t>(h) * D, e, a.rot,
+                        a.inter, cs + r * half, y);
+            store8(static_cast<T *>(a.q_out) + (static_cast<size_t>(tok + r) * a.hq + h) * D + e, y);
+          }
+        }
+      }
+    }
+    __syncthreads();  // the table of sines is read
+  }
+  pdl_trigger();
+  if (a.advance) {
+    // every CTA has read the lengths: the last to arrive advances them
+    __shared__ int last_s;
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      const uint32_t all = gridDim.x * gridDim.y;
+      last_s = atomicAdd(a.counter, 1u) == all - 1;
+      if (last_s) {
+        __threadfence();
+        *a.counter = 0u;
+      }
+    }
+    __syncthreads();
+    if (last_s)
+      for (int b = tid; b < a.B; b += kApThreads) {
+        int start, tok0;
+        const int n = append_span(a, b, start, tok0);
+        if (n > 0) a.own_len[b] = max(__ldcg(a.own_len + b), 0) + n;
+      }
+  }
+}
+
+}  // namespace gsa
