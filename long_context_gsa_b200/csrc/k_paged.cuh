@@ -7,35 +7,40 @@
 //
 // The product kernel of both readers (k_paged_attend: all rows of a
 // sequence; k_paged_unfold: selected chunks and the own chunk of one query
-// head) is one warp working through tiles of 16 rows:
-//   z  = K q       S^T[16 keys x 8 queries], mma.sync m16n8k16 with the KEYS
-//                  as the A operand: a kv head's 4..8 query heads fill the 8
-//                  columns, where queries as A would leave 8..12 of 16 rows
-//                  idle;
-//   p  = 2^(z - m) lazy online softmax in fp32 (m raised when exceeded by
-//                  kPgSlack), the scale of K applied to z;
-//   O^T += V^T p   m16n8k16 with V^T as A (the tile's codes, transposed by
-//                  byte permutes in registers) and p as B (movmatrix turns the
-//                  accumulator layout of S^T into it).
-// 8-bit codes are exact in fp16 (int8: |c| <= 127, e4m3: 4 significant bits
-// within fp16's range), so K enters exactly.  Queries enter as fp16 after a
-// power-of-two scaling of each row to [2^14, 2^15): exact for bf16 within 2^-38
-// of the row's maximum; fp32 queries enter as two fp16 terms (22 bits).  p
-// enters as one fp16 term when the output is bf16 (2^-12 relative, against
-// the 2^-9 of the output's own rounding) and as two (2^-22) when it is
-// fp32; the scale of V goes into p relative to the tile's largest scale,
-// which is applied to the tile's product in fp32.  Statistics, sums and the
-// running output are fp32.
+// head) is one warp working through tiles of 32 rows:
+//   z = K q        S^T[16 keys x 8 queries], mma.sync m16n8k32 on the codes as
+//                  they are, the KEYS as the A operand: a kv head's 4..8 query
+//                  heads fill the 8 columns, where queries as A would leave
+//                  8..12 of 16 rows idle;
+//   p = 2^(z - m)  lazy online softmax in fp32 (m raised when exceeded by
+//                  kPgSlack), the scale of K applied to z, that of V to p;
+//   O^T += V^T p   m16n8k32 with V^T as A (4 x 4 byte transposes of the codes
+//                  in registers) and p as B (movmatrix turns the accumulator
+//                  layout of S^T into it).
+// The 8-bit operands of the other side are written as sums of 8-bit digits,
+// one product each, so the codes need no conversion:
+//   e4m3 (4 significant bits a digit): a bf16 query is 2 digits, the second
+//     in an accumulator of its own at 2^4 times the scale; an fp32 one 3 + 3 at
+//     2^12.  A row is scaled by a power of two so that its largest element
+//     lies in [128, 256): digits end at 2^-10, 2^-22 (2^-30) of it.
+//   int8 (7 bits a digit, fixed point): 3 digits for bf16 queries (2^-20 of the
+//     row's largest element), 4 for fp32 (2^-28); sums are exact integers.
+//   p times the scale of V is scaled by the largest of the tile's 32 in its
+//     column: e4m3 3 digits (2^-12 of the weight, 2^-18 of the largest) or 6
+//     (2^-22, 2^-30), int8 2 digits (2^-15 of the largest) or 3 (2^-22): the
+//     fewer for bf16 outputs, whose own rounding is 2^-8.
+// Statistics, sums of weights and the running output are fp32.
 //
 // What bounds it: HBM reads of the codes.  Every warp copies its tiles with
 // 16-byte cp.async into its own ring, so there is no CTA-wide barrier in
-// the loop and 2 tiles of 4 KB (d = 128) or 4 of 2 KB (d = 64) are in flight
-// for each of 16 warps on an SM; page-table entries are fetched one tile
-// ahead of the copies, scales one tile behind them.
+// the loop; page-table entries are fetched one tile ahead of the copies,
+// scales one tile behind them.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
-#include "k_unfold.cuh"  // UnfoldArgs, ready list, combine of partial records
+#include "k_unfold.cuh"  // UnfoldArgs, ready list
 
 namespace gsa {
 
@@ -63,8 +68,7 @@ struct PagedKV {
   FastDiv page, chunk;
 };
 
-constexpr float kPgSlack = 4.0f;     // p <= 2^4 before the reference is raised
-constexpr float kPgPScale = 2048.f;  // p is scaled by 2^11 into fp16's range (<= 2^15)
+constexpr float kPgSlack = 16.0f;  // p <= 2^16 before the reference is raised (p is fp32)
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -75,27 +79,69 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma_16816_f16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
+// c += A B on 8-bit codes (16 x 32 times 32 x 8).
+__device__ __forceinline__ void mma_16832(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ void mma_16832(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
 
-// 8x8 fp16 block transposed across the warp's accumulator layout.
+// 8x8 block of 16-bit elements transposed across the warp's accumulator layout.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
+
+// (a.x * b.x + c.x, a.y * b.y + c.y)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)),
+        "l"(*reinterpret_cast<const uint64_t *>(&c)));
+  return *reinterpret_cast<const float2 *>(&r);
+}
+
 __device__ __forceinline__ float2 unpack_h2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// e4m3 pair (16 bits) of an fp16 pair, and back.
+__device__ __forceinline__ uint16_t h2_to_e4(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+  return r;
+}
+__device__ __forceinline__ __half2 e4_to_h2(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return *reinterpret_cast<const __half2 *>(&r);
+}
+
+// N e4m3 digits of an fp16 pair: out[i] is the rounding of what out[0..i-1] left.  Returns the remainder (exact).
+template <int N>
+__device__ __forceinline__ __half2 e4_digits(__half2 x, uint16_t *out) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    out[i] = h2_to_e4(x);
+    x = __hsub2(x, e4_to_h2(out[i]));
+  }
+  return x;
 }
 
 // Four codes -> two fp16 pairs (bytes 0,1 and bytes 2,3), exact.
@@ -111,107 +157,163 @@ __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t &lo, uint32_t &
     lo = *reinterpret_cast<const uint32_t *>(&x);
     hi = *reinterpret_cast<const uint32_t *>(&y);
   } else {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
+    const __half2 x = e4_to_h2(static_cast<uint16_t>(w)), y = e4_to_h2(static_cast<uint16_t>(w >> 16));
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
   }
 }
 
 // One warp's ring: per stage K as [slot][lane] 16-byte pieces (each lane
-// reads back what it copied), V as 16 rows with swizzled 16-byte pieces, the
-// 32 scales of the tile (K then V) and the mask of live keys.
+// reads back what it copied), V as 32 rows with swizzled 16-byte pieces, the
+// 64 scales of the tile (K then V) and the mask of live keys.
 template <int D>
 struct PgCfg {
-  static constexpr int kStages = D == 64 ? 5 : 3;
-  static constexpr uint32_t kK = 16 * D, kV = 16 * D;
-  static constexpr uint32_t kStage = kK + kV + 32 * 4 + 16;
+  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kCtas = D == 64 ? 4 : 3;  // of 4 warps on an SM
+  static constexpr uint32_t kK = 32 * D, kScales = 64 * D, kMask = kScales + 256;
+  static constexpr uint32_t kStage = kMask + 16;
   static constexpr uint32_t kRing = kStages * kStage;
 };
 
 // Offset of 16-byte piece p of row r inside a stage's V: lanes (g, t) read
-// rows 2t (+1, +8, +9) at dims g*D/8.., and the permutations below spread the
-// 8 lanes of a shared-memory phase over all 32 banks.
+// rows 2t (+1, +8, +9, ..) at dims g*D/8.., and the permutations below spread
+// the 8 lanes of a shared-memory phase over all 32 banks.
 template <int D>
 __device__ __forceinline__ uint32_t v_off(uint32_t r, uint32_t p) {
   if (D == 128) return r * 128 + ((p ^ (((r >> 1) & 3) << 1)) << 4);
   return (r ^ ((r >> 2) & 1)) * 64 + ((p ^ (((r >> 1) & 1) << 1)) << 4);
 }
 
+// Digits of the queries: how many, and how they group into two accumulators
+// (the value is acc[0] + acc[1] * kRest for e4m3, acc[0] * kTop + acc[1] for
+// int8, whose first digits come first).
+template <int FMT, bool QF32>
+struct QDigits {
+  static constexpr int kFirst = FMT == kFmtI8 ? 2 : (QF32 ? 3 : 1);  // digits of acc[0]
+  static constexpr int kN = FMT == kFmtI8 ? (QF32 ? 4 : 3) : 2 * kFirst;
+  static constexpr float kUp = QF32 ? 4096.f : 16.f;   // e4m3: scale of the second group
+  static constexpr int kBits = 7 * kN - 1;             // int8: |fixed point| < 2^kBits
+  static constexpr float kTop = kN == 4 ? 16384.f : 128.f;
+};
+
+// The queries of a segment in shared memory, as the B fragments of their
+// digits: [NT][digit][k-step of 32 dims][lane], and the factor of each row's
+// logits.  Row n (< 8 NT) is row(n), null when unused.
+template <int D, int FMT, bool QF32, int NT>
+struct PgQuery {
+  using Dg = QDigits<FMT, QF32>;
+  static constexpr int KS = D / 32;
+  uint2 frag[NT][Dg::kN][KS][32];
+  float f[8 * NT];
+
+  // Group nt, by one warp.
+  template <typename RowFn>
+  __device__ __forceinline__ void load(int nt, RowFn row, float scale_log2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const void *p = row(8 * nt + g);
+    float x[D / 4];  // dims 64 c + 16 t + 0..15
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+      for (int v = 0; v < (QF32 ? 4 : 2); ++v) {
+        const int e = (c * 64 + t * 16) + v * (QF32 ? 4 : 8);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (p) w = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + e * (QF32 ? 4 : 2)));
+        if (QF32)
+          Vec16<float>::unpack(w, x + c * 16 + v * 4);
+        else
+          Vec16<__nv_bfloat16>::unpack(w, x + c * 16 + v * 8);
+      }
+    }
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) a = max(a, __float_as_uint(x[i]) & 0x7fffffffu);
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    // power of two that brings the row's maximum into [2^(top-1), 2^top); none for a row of zeros.  An inf or NaN
+    // makes the row's logits NaN.
+    constexpr int kTopExp = FMT == kFmtI8 ? Dg::kBits : 8;
+    int sh = 0;
+    if (a != 0 && a < 0x7f800000u) sh = min(kTopExp - 1 - (static_cast<int>(a >> 23) - 127), 120);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * scale_log2;
+    if (t == 0) f[8 * nt + g] = a < 0x7f800000u ? down : __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      // words of b0 (dims 8 s' + 0..3) and b1 (+ 4..7) of this k-step
+      uint32_t w[Dg::kN][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float *y = x + 8 * s + 4 * h;
+        if (FMT == kFmtI8) {
+          uint32_t d[Dg::kN][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            int v = __float2int_rn(y[i] * up);
+#pragma unroll
+            for (int k = Dg::kN - 1; k >= 0; --k) {  // last digit first; each in [-64, 63], the first takes the rest
+              const int top = k == 0 ? v : ((v + 64) & 127) - 64;
+              d[k][i] = static_cast<uint32_t>(top) & 0xffu;
+              v = (v - top) >> 7;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < Dg::kN; ++k) w[k][h] = d[k][0] | d[k][1] << 8 | d[k][2] << 16 | d[k][3] << 24;
+        } else {
+          uint16_t d[2][Dg::kN];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float u = y[2 * i] * up, v = y[2 * i + 1] * up;
+            const __half2 r = __floats2half2_rn(u, v);  // exact for bf16 down to fp16's subnormals
+            const float2 rf = __half22float2(r);
+            const float2 left = __half22float2(e4_digits<Dg::kFirst>(r, d[i]));
+            e4_digits<Dg::kN - Dg::kFirst>(
+                __floats2half2_rn(((u - rf.x) + left.x) * Dg::kUp, ((v - rf.y) + left.y) * Dg::kUp),
+                d[i] + Dg::kFirst);
+          }
+#pragma unroll
+          for (int k = 0; k < Dg::kN; ++k) w[k][h] = d[0][k] | static_cast<uint32_t>(d[1][k]) << 16;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < Dg::kN; ++k) frag[nt][k][s][lane] = make_uint2(w[k][0], w[k][1]);
+    }
+  }
+};
+
 // The state of one warp over a run of tiles; NT groups of 8 query columns.
 template <int D, int FMT, bool QF32, bool HILO, int NT>
 struct PgWarp {
   using Cfg = PgCfg<D>;
+  using Query = PgQuery<D, FMT, QF32, NT>;
+  using Dg = QDigits<FMT, QF32>;
+  using Acc = typename std::conditional<FMT == kFmtI8, int, float>::type;
   static constexpr int S = Cfg::kStages;
-  static constexpr int KS = D / 16;          // k-steps of S^T, m-tiles of O^T
-  static constexpr int QT = QF32 ? 2 : 1;    // fp16 terms of a query element
+  static constexpr int MT = D / 16;  // m-tiles of O^T
+  // digits of a weight; int8: the first two share an accumulator
+  static constexpr int PN = FMT == kFmtI8 ? (HILO ? 3 : 2) : (HILO ? 6 : 3);
+  static constexpr float kPTop = FMT == kFmtI8 ? (HILO ? 2080768.f : 16256.f) : 448.f;  // 127 * 2^7 or 2^14
 
-  uint32_t qf[QT][NT][KS][2];  // B fragments of the queries
-  float f[NT][2];              // z factor of this lane's columns 2t, 2t + 1
-  float m[NT][2], l[NT][2];
-  float o[NT][KS][4];          // O^T: dims g*D/8 + 2j (+1), columns 2t, 2t + 1
+  float m[NT][2], l[NT][2];  // columns 2t, 2t + 1
+  float2 o[NT][MT][2];       // O^T: dims g*D/8 + 2j and + 2j + 1, (column 2t, column 2t + 1)
   // the copy pipeline
-  int32_t pid;                 // page of this lane's key in the next tile to copy (-1: none)
-  uint32_t off;                // its row in that page
-  float sc;                    // scale of the tile copied last (K: lanes 0..15, V: lanes 16..31)
+  int32_t pid;     // page of this lane's key in the next tile to copy (-1: none)
+  uint32_t off;    // its row in that page
+  float sck, scv;  // scales of this lane's key in the tile copied last
   uint32_t ring;
 
-  // Query column n (0 .. 8 NT - 1) is row(n), null when unused.
-  template <typename RowFn>
-  __device__ __forceinline__ void load_q(RowFn row, float scale_log2) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const void *p = row(8 * nt + g);
-      float x[D / 4];
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-        for (int v = 0; v < (QF32 ? 4 : 2); ++v) {
-          const int e = (c * 64 + t * 16) + v * (QF32 ? 4 : 8);
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (p) w = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + e * (QF32 ? 4 : 2)));
-          if (QF32)
-            Vec16<float>::unpack(w, x + c * 16 + v * 4);
-          else
-            Vec16<__nv_bfloat16>::unpack(w, x + c * 16 + v * 8);
-        }
-      }
-      uint32_t a = 0;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) a = max(a, __float_as_uint(x[i]) & 0x7fffffffu);
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      // exponent shift that brings the row's maximum into [2^14, 2^15); none for zero, inf or NaN rows
-      int sh = 0;
-      if (a != 0 && a < 0x7f800000u) sh = min(14 - (static_cast<int>(a >> 23) - 127), 120);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * scale_log2;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x0 = x[4 * s + 2 * h] * up, x1 = x[4 * s + 2 * h + 1] * up;
-          qf[0][nt][s][h] = pack_h2(x0, x1);
-          if (QF32) {
-            const float2 r = unpack_h2(qf[0][nt][s][h]);
-            qf[QT - 1][nt][s][h] = pack_h2(x0 - r.x, x1 - r.y);
-          }
-        }
-      f[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-      f[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
       m[nt][0] = m[nt][1] = neg_inf();
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int j = 0; j < KS; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+      for (int j = 0; j < MT; ++j) o[nt][j][0] = o[nt][j][1] = make_float2(0.f, 0.f);
     }
   }
 
-  // Fetch the page of raw row r (< 0: no such key); lanes 16..31 hold the
-  // same keys as lanes 0..15.
-  __device__ __forceinline__ void fetch(const PagedKV &kv, const int32_t *table, int64_t r) {
+  // Fetch the page of raw row r (< 0: no such key).
+  __device__ __forceinline__ void fetch(const PagedKV &kv, const int32_t *table, int r) {
     pid = -1;
     off = 0;
     if (r >= 0) {
@@ -226,16 +328,20 @@ struct PgWarp {
   __device__ __forceinline__ void copy(const PagedKV &kv, int kvh, int st, bool wanted, uint32_t *status) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const bool live = static_cast<uint32_t>(pid) < static_cast<uint32_t>(kv.n_pages);
-    if (wanted && !live && lane < 16) flag_error(status, GSA_DEVERR_BAD_INDEX);
+    if (wanted && !live) flag_error(status, GSA_DEVERR_BAD_INDEX);
     const uint32_t ph = live ? static_cast<uint32_t>(pid) * kv.hkv + kvh : 0u;
     const uint32_t prow = live ? ph * kv.page.d + off : 0xffffffffu;
-    sc = 0.f;
-    if (live) sc = __ldcg((lane < 16 ? kv.ks : kv.vs) + (static_cast<size_t>(ph) * kv.blocks + kv.chunk.div(off)));
+    sck = scv = 0.f;
+    if (live) {
+      const size_t i = static_cast<size_t>(ph) * kv.blocks + kv.chunk.div(off);
+      sck = __ldcg(kv.ks + i);
+      scv = __ldcg(kv.vs + i);
+    }
     const uint32_t base = ring + st * Cfg::kStage;
-    const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
-    if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + 32 * D + 128), "r"(mask) : "memory");
+    const uint32_t mask = __ballot_sync(0xffffffffu, live);
+    if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + Cfg::kMask), "r"(mask) : "memory");
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // keys g and g + 8
+    for (int i = 0; i < 4; ++i) {  // keys g + 8 i
       const uint32_t r = __shfl_sync(0xffffffffu, prow, g + 8 * i);
       const uint32_t bytes = r != 0xffffffffu ? 16u : 0u;
       const size_t o8 = bytes ? static_cast<size_t>(r) * D + t * 16 : 0;
@@ -248,153 +354,254 @@ struct PgWarp {
   }
 
   __device__ __forceinline__ void put_scale(int st) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + st * Cfg::kStage + 32 * D + (threadIdx.x & 31) * 4), "f"(sc)
-                 : "memory");
+    const uint32_t at = ring + st * Cfg::kStage + Cfg::kScales + (threadIdx.x & 31) * 4;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(sck) : "memory");
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128), "f"(scv) : "memory");
   }
 
-  // Work through tile i in stage st; key0: index of its first key, lim:
-  // columns 2t, 2t+1 see keys below lim (CAUSAL).
+  __device__ __forceinline__ static void lds4(uint32_t at, uint32_t *w) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+  }
+  __device__ __forceinline__ static float ldsf(uint32_t at) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+  }
+
+  // Work through the tile in stage st; key0: index of its first key, lim:
+  // columns 2t, 2t + 1 see keys below lim (CAUSAL).
   template <bool CAUSAL>
-  __device__ __forceinline__ void step(int st, int64_t key0, const int64_t (*lim)[2]) {
+  __device__ __forceinline__ void step(const Query &qs, int st, int key0, const int (*lim)[2]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t base = ring + st * Cfg::kStage, scb = base + 32 * D;
-    float kg[2], vg[2];
+    const uint32_t base = ring + st * Cfg::kStage, scb = base + Cfg::kScales + 4 * g;
     uint32_t mask;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kg[0]) : "r"(scb + 4 * g));
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kg[1]) : "r"(scb + 4 * g + 32));
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vg[0]) : "r"(scb + 4 * g + 64));
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vg[1]) : "r"(scb + 4 * g + 96));
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(scb + 128));
-    float z[NT][4];
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(base + Cfg::kMask));
+    // ---- z: value e of half h: key 16 h + g + 8 (e >> 1), column 2 t + (e & 1)
+    float z[2][NT][4];
+    {
+      Acc acc[2][NT][2][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      uint32_t a[4], b[4];
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                   : "r"(base + (c * 32 + lane) * 16));
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                   : "r"(base + ((D / 64 + c) * 32 + lane) * 16));
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t a0, a1, a2, a3;
-        codes_to_h2<FMT>(a[w], a0, a2);
-        codes_to_h2<FMT>(b[w], a1, a3);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int q = 0; q < QT; ++q)
-            mma_16816_f16(z[nt], a0, a1, a2, a3, qf[q][nt][c * 4 + w][0], qf[q][nt][c * 4 + w][1]);
-      }
-    }
-    const bool live0 = (mask >> g) & 1u, live1 = (mask >> (g + 8)) & 1u;
-    bool over = false;
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 4; ++e) acc[h][nt][k][e] = 0;
+      uint32_t kw[D / 64][4][4];  // [piece][row g + 8 i][word]
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        bool see = e < 2 ? live0 : live1;
-        if (CAUSAL) see = see && key0 + g + (e < 2 ? 0 : 8) < lim[nt][e & 1];
-        z[nt][e] = see ? z[nt][e] * (kg[e >> 1] * f[nt][e & 1]) : neg_inf();
-        over = over || z[nt][e] > m[nt][e & 1] + kPgSlack;
-      }
-    if (__any_sync(0xffffffffu, over)) {  // raise the references, rescale
+      for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 4; ++i) lds4(base + ((i * (D / 64) + c) * 32 + lane) * 16, kw[c][i]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float mx = fmaxf(z[nt][x], z[nt][x + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (mx > m[nt][x]) {
-            const float c = exp2_approx(m[nt][x] - mx);  // 0 when there was no reference
-            l[nt][x] *= c;
+      for (int k = 0; k < Dg::kN; ++k) {
+        const int group = k < Dg::kFirst ? 0 : 1;
+        if (FMT == kFmtI8 && k == (group ? Dg::kFirst + 1 : 1)) {  // second digit of its accumulator
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-              o[nt][j][x] *= c;
-              o[nt][j][x + 2] *= c;
-            }
-            m[nt][x] = mx;
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[h][nt][group][e] *= 128;
         }
-    }
-    // the scale of V relative to the tile's largest (scales are >= 0, so their bits order like the values; fmaxf
-    // drops a NaN scale here, which then reaches only the columns that see its keys)
-    const float vmax =
-        __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(vg[0], vg[1]), 0.f))));
-    const float inv = vmax != 0.f ? __fdividef(kPgPScale, vmax) : 0.f;
-    const float w0 = vg[0] * inv, w1 = vg[1] * inv;
-    uint32_t pb[HILO ? 2 : 1][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float p[4];
+        for (int s = 0; s < D / 32; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float mm = m[nt][e & 1];
-        p[e] = exp2_approx(z[nt][e] - (mm == neg_inf() ? 0.f : mm));
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = qs.frag[nt][k][s][lane];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_16832(acc[h][nt][group], kw[s / 2][2 * h][2 * (s & 1)], kw[s / 2][2 * h + 1][2 * (s & 1)],
+                        kw[s / 2][2 * h][2 * (s & 1) + 1], kw[s / 2][2 * h + 1][2 * (s & 1) + 1], b);
+          }
       }
-      l[nt][0] += p[0] + p[2];
-      l[nt][1] += p[1] + p[3];
+      bool over = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = z[nt][e] == neg_inf() ? 0.f : p[e] * (e < 2 ? w0 : w1);
-      const uint32_t h0 = pack_h2(p[0], p[1]), h1 = pack_h2(p[2], p[3]);
-      pb[0][nt][0] = movmatrix_trans(h0);
-      pb[0][nt][1] = movmatrix_trans(h1);
-      if (HILO) {
-        const float2 r0 = unpack_h2(h0), r1 = unpack_h2(h1);
-        pb[HILO ? 1 : 0][nt][0] = movmatrix_trans(pack_h2(p[0] - r0.x, p[1] - r0.y));
-        pb[HILO ? 1 : 0][nt][1] = movmatrix_trans(pack_h2(p[2] - r1.x, p[3] - r1.y));
-      }
-    }
-    const float back = vmax * (1.f / kPgPScale);
-    constexpr int kW = D / 32;  // 32-bit words of a lane's D/8 codes of one row
-    uint32_t vr[4][kW];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = 2 * t + (i & 1) + 8 * (i >> 1);
-      if (D == 128)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(vr[i][0]), "=r"(vr[i][1]), "=r"(vr[i][kW - 2]), "=r"(vr[i][kW - 1])
-                     : "r"(base + Cfg::kK + v_off<D>(r, g)));
-      else
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(vr[i][0]), "=r"(vr[i][1])
-                     : "r"(base + Cfg::kK + v_off<D>(r, g >> 1) + (g & 1) * 8));
-    }
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      // (row 2t, row 2t+1) pairs of each dim, then rows 2t+8, 2t+9
-      uint32_t a[2][2], c[2][2];
-      codes_to_h2<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
-      codes_to_h2<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
-      codes_to_h2<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x5140), c[0][0], c[0][1]);
-      codes_to_h2<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x7362), c[1][0], c[1][1]);
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int h = 0; h < 2; ++h) {
+        const float kg[2] = {ldsf(scb + 64 * h), ldsf(scb + 64 * h + 32)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16816_f16(d, a[x][0], a[x][1], c[x][0], c[x][1], pb[0][nt][0], pb[0][nt][1]);
-          if (HILO)
-            mma_16816_f16(d, a[x][0], a[x][1], c[x][0], c[x][1], pb[HILO ? 1 : 0][nt][0], pb[HILO ? 1 : 0][nt][1]);
+          const float2 f = *reinterpret_cast<const float2 *>(&qs.f[8 * nt + 2 * t]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][2 * w + x][e] = fmaf(back, d[e], o[nt][2 * w + x][e]);
+          for (int e = 0; e < 4; ++e) {
+            const float v = FMT == kFmtI8 ? fmaf(static_cast<float>(acc[h][nt][0][e]), Dg::kTop,
+                                                 static_cast<float>(acc[h][nt][1][e]))
+                                          : fmaf(static_cast<float>(acc[h][nt][1][e]), 1.f / Dg::kUp,
+                                                 static_cast<float>(acc[h][nt][0][e]));
+            const int key = 16 * h + g + 8 * (e >> 1);
+            bool see = (mask >> key) & 1u;
+            if (CAUSAL) see = see && key0 + key < lim[nt][e & 1];
+            z[h][nt][e] = see ? v * (kg[e >> 1] * (e & 1 ? f.y : f.x)) : neg_inf();
+            over = over || z[h][nt][e] > m[nt][e & 1] + kPgSlack;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, over)) {  // raise the references, rescale
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = fmaxf(fmaxf(z[0][nt][x], z[0][nt][x + 2]), fmaxf(z[1][nt][x], z[1][nt][x + 2]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            c[x] = mx > m[nt][x] ? exp2_approx(m[nt][x] - mx) : 1.f;  // 0 when there was no reference
+            l[nt][x] *= c[x];
+            m[nt][x] = fmaxf(m[nt][x], mx);
+          }
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              o[nt][j][y].x *= c[0];
+              o[nt][j][y].y *= c[1];
+            }
+        }
+      }
+    }
+    // ---- weights: p, times the scale of V, relative to the column's largest of the tile; their digits as B fragments
+    uint2 pb[PN][NT];
+    float2 back[NT];
+    float vg[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vg[i] = ldsf(scb + 128 + 32 * i);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[2][4], top[2];
+      const float m0 = m[nt][0] == neg_inf() ? 0.f : m[nt][0], m1 = m[nt][1] == neg_inf() ? 0.f : m[nt][1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp2_approx(z[h][nt][e] - (e & 1 ? m1 : m0));
+          l[nt][e & 1] += p;
+          w[h][e] = z[h][nt][e] == neg_inf() ? 0.f : p * vg[2 * h + (e >> 1)];  // (a scale of NaN stays with its keys)
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float a = max_nan(max_nan(w[0][x], w[0][x + 2]), max_nan(w[1][x], w[1][x + 2]));
+        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 4));
+        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        top[x] = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 16));
+      }
+      // (weights whose reciprocal fp32 does not hold, below kPTop 2^-126, are zero)
+      const float i0 = top[0] > kPTop * 1.18e-38f ? __fdividef(kPTop, top[0]) : 0.f;
+      const float i1 = top[1] > kPTop * 1.18e-38f ? __fdividef(kPTop, top[1]) : 0.f;
+      back[nt] = make_float2(top[0] * (1.f / kPTop), top[1] * (1.f / kPTop));
+      // 16-bit element (key g, column): digits of keys g and g + 8 of the half
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t dig[PN];
+        if (FMT == kFmtI8) {
+          int v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = __float2int_rn(w[h][e] * (e & 1 ? i1 : i0));
+#pragma unroll
+          for (int k = PN - 1; k >= 0; --k) {
+            // bytes: column 2t (keys g, g + 8), column 2t + 1 (keys g, g + 8); the last digit in [-64, 63]
+            int r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              r[e] = k == 0 ? v[e] : v[e] + 64;
+              v[e] = r[e] >> 7;
+              if (k > 0) r[e] = (r[e] & 127) - 64;
+            }
+            dig[k] = __byte_perm(__byte_perm(r[0], r[2], 0x0040), __byte_perm(r[1], r[3], 0x0040), 0x5410);
+          }
+        } else {
+          uint16_t d0[PN], d1[PN];
+          const float a0 = w[h][0] * i0, a2 = w[h][2] * i0, b0 = w[h][1] * i1, b2 = w[h][3] * i1;
+          const __half2 ha = __floats2half2_rn(a0, a2), hb = __floats2half2_rn(b0, b2);
+          const __half2 ra = e4_digits<3>(ha, d0), rb = e4_digits<3>(hb, d1);
+          if (HILO) {
+            const float2 fa = __half22float2(ha), fb = __half22float2(hb);
+            const float2 la = __half22float2(ra), lb = __half22float2(rb);
+            e4_digits<3>(__floats2half2_rn(((a0 - fa.x) + la.x) * 4096.f, ((a2 - fa.y) + la.y) * 4096.f),
+                         d0 + (HILO ? 3 : 0));
+            e4_digits<3>(__floats2half2_rn(((b0 - fb.x) + lb.x) * 4096.f, ((b2 - fb.y) + lb.y) * 4096.f),
+                         d1 + (HILO ? 3 : 0));
+          }
+#pragma unroll
+          for (int k = 0; k < PN; ++k) dig[k] = d0[k] | static_cast<uint32_t>(d1[k]) << 16;
+        }
+#pragma unroll
+        for (int k = 0; k < PN; ++k) (h ? pb[k][nt].y : pb[k][nt].x) = movmatrix_trans(dig[k]);
+      }
+    }
+    // ---- O^T += V^T p: dims in words of 4 codes, rows 2t, 2t+8, 2t+1, 2t+9 of each half
+    constexpr int kW = D / 32;
+    uint32_t vr[2][4][kW];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t r = 16 * h + 2 * t + (i >> 1) + 8 * (i & 1);
+        if constexpr (D == 128) {
+          lds4(base + Cfg::kK + v_off<D>(r, g), vr[h][i]);
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                       : "=r"(vr[h][i][0]), "=r"(vr[h][i][1])
+                       : "r"(base + Cfg::kK + v_off<D>(r, g >> 1) + (g & 1) * 8));
+        }
+      }
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      uint32_t a[2][4];  // [half][dim]: four keys' codes
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = __byte_perm(vr[h][0][w], vr[h][1][w], 0x5140);
+        const uint32_t y = __byte_perm(vr[h][0][w], vr[h][1][w], 0x7362);
+        const uint32_t u = __byte_perm(vr[h][2][w], vr[h][3][w], 0x5140);
+        const uint32_t v = __byte_perm(vr[h][2][w], vr[h][3][w], 0x7362);
+        a[h][0] = __byte_perm(x, u, 0x5410);
+        a[h][1] = __byte_perm(x, u, 0x7632);
+        a[h][2] = __byte_perm(y, v, 0x5410);
+        a[h][3] = __byte_perm(y, v, 0x7632);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          constexpr int kAcc = HILO ? 2 : 1;
+          Acc d[kAcc][4];
+#pragma unroll
+          for (int k = 0; k < kAcc; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[k][e] = 0;
+#pragma unroll
+          for (int k = 0; k < PN; ++k) {
+            const int group = FMT == kFmtI8 ? k / 2 : k / 3;
+            if (FMT == kFmtI8 && k == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[0][e] *= 128;
+            }
+            mma_16832(d[group], a[0][2 * j], a[0][2 * j + 1], a[1][2 * j], a[1][2 * j + 1], pb[k][nt]);
+          }
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = static_cast<float>(d[0][e]);
+            if (HILO)
+              v[e] = FMT == kFmtI8 ? fmaf(v[e], 128.f, static_cast<float>(d[kAcc - 1][e]))
+                                   : fmaf(static_cast<float>(d[kAcc - 1][e]), 1.f / 4096.f, v[e]);
+          }
+          o[nt][2 * w + j][0] = fma2(back[nt], make_float2(v[0], v[1]), o[nt][2 * w + j][0]);
+          o[nt][2 * w + j][1] = fma2(back[nt], make_float2(v[2], v[3]), o[nt][2 * w + j][1]);
         }
     }
   }
 
-  // Run n tiles; raw(i) is this lane's key (lane & 15) of tile i as a raw row
-  // (< 0: none), key0(i) the index of the tile's first key; before() runs once
-  // while the first copies are in flight.
+  // Run n tiles; raw(i) is this lane's key of tile i as a raw row (< 0:
+  // none), key0(i) the index of the tile's first key; before() runs once
+  // while the first copies are in flight (and makes qs ready).
   template <bool CAUSAL, typename RawFn, typename Key0Fn, typename BeforeFn>
-  __device__ __forceinline__ void run(const PagedKV &kv, const int32_t *table, int kvh, int n, RawFn raw, Key0Fn key0,
-                                      const int64_t (*lim)[2], uint32_t *status, BeforeFn before) {
-    int64_t r = n > 0 ? raw(0) : -1;
+  __device__ __forceinline__ void run(const PagedKV &kv, const int32_t *table, int kvh, int n, const Query &qs,
+                                      RawFn raw, Key0Fn key0, const int (*lim)[2], uint32_t *status, BeforeFn before) {
+    clear();
+    int r = n > 0 ? raw(0) : -1;
     fetch(kv, table, r);
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
@@ -419,7 +626,7 @@ struct PgWarp {
         fetch(kv, table, r);
       }
       cp_async_commit();
-      step<CAUSAL>(st, key0(i), lim);
+      step<CAUSAL>(qs, st, key0(i), lim);
       st = st == S - 1 ? 0 : st + 1;
       stc = stc == S - 1 ? 0 : stc + 1;
     }
@@ -438,16 +645,17 @@ struct PgWarp {
 
 // ------------------------------------------------------------ dense attention
 // The rows of all (sequence, kv head, group of 8 NT query rows) segments, in
-// steps of 16 rows a warp, form one line that the CTAs cut into equal parts
+// steps of 32 rows a warp, form one line that the CTAs cut into equal parts
 // (the lengths are on the device, so the cut is too): ragged batches and
 // single long sequences load every SM alike.  A segment inside one CTA is
 // written directly; one that several CTAs share is joined by the last of them
 // to arrive (an atomic counter, no waiting) from partial records, in CTA
-// order, so the result does not depend on who was last.
-constexpr int kPgWarps = 8;
+// order, so the result does not depend on who was last.  CTAs of 4 warps, 3
+// or 4 on an SM: one joins its warps while the others stream.
+constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
-constexpr int kPgStep = 16 * kPgWarps;  // rows of one CTA step
-constexpr int kPgMaxCtas = 1024;        // bound of the grid (partial slots in the workspace)
+constexpr int kPgStep = 32 * kPgWarps;  // rows of one CTA step
+constexpr int kPgMaxCtas = 640;         // bound of the grid (partial slots in the workspace)
 constexpr int kPgMaxBatch = 8192;       // prefix sums in shared memory
 constexpr int kPgMaxRows = 16;          // query rows of a segment
 
@@ -514,18 +722,25 @@ __device__ __forceinline__ int paged_find(const uint32_t *pre, int B, uint32_t p
   return lo;
 }
 
-template <int D, int NT>
+// Dynamic shared memory: rings (over them, once drained, the warps' results
+// and the weights of a join) | queries | prefix sums [B + 1] and lengths [B].
+template <int D, int FMT, bool QF32, int NT>
 __host__ __device__ constexpr uint32_t paged_attend_smem() {
-  return kPgWarps * (PgCfg<D>::kRing > 8 * NT * (D + 4) * 4 ? PgCfg<D>::kRing : 8 * NT * (D + 4) * 4);
+  return kPgWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, NT>);
 }
 
 template <int D, int FMT, bool QF32, bool HILO, int NT>
-__global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_attend(const PagedAttendArgs a) {
+__global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(const PagedAttendArgs a) {
   using Warp = PgWarp<D, FMT, QF32, HILO, NT>;
+  using Query = typename Warp::Query;
   constexpr int R = 8 * NT, kRec = D + kPartHeader;
+  static_assert(kPgWarps * PgCfg<D>::kRing >= (kPgWarps * R * kRec + 4 * kPgThreads) * 4, "results fit over the rings");
+  static_assert(kPgWarps * PgCfg<D>::kRing >= (R * kPgMaxCtas + 4 * kPgThreads) * 4, "a join fits over the rings");
   extern __shared__ __align__(128) uint8_t smem[];
-  uint32_t *pre = reinterpret_cast<uint32_t *>(smem + paged_attend_smem<D, NT>());
-  float(*red)[R][kRec] = reinterpret_cast<float(*)[R][kRec]>(smem);  // over the rings, once they are drained
+  Query &qs = *reinterpret_cast<Query *>(smem + kPgWarps * PgCfg<D>::kRing);
+  uint32_t *pre = reinterpret_cast<uint32_t *>(smem + paged_attend_smem<D, FMT, QF32, NT>());
+  int *lens = reinterpret_cast<int *>(pre + a.B + 1);
+  float(*red)[R][kRec] = reinterpret_cast<float(*)[R][kRec]>(smem);
   __shared__ float wgt[R][kPgWarps], rowM[R], rowL[R];
   __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -533,6 +748,7 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
   pdl_wait();
   paged_prefix<kPgThreads>(pre, a.B, [&](int b) {
     const int len = paged_len(a.n_gists, a.own_len, b, a.n_max, a.chunk, a.t_max);
+    lens[b] = len;
     return static_cast<uint32_t>(per_b) * static_cast<uint32_t>((len + kPgStep - 1) / kPgStep);
   });
   const uint32_t total = pre[a.B];
@@ -540,7 +756,7 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
   const uint32_t cta = blockIdx.x;
   // sequences without rows: zeros, ln of an empty sum
   for (int b = cta; b < a.B; b += gridDim.x)
-    if (pre[b] == pre[b + 1]) {
+    if (lens[b] == 0) {
       const size_t row0 = static_cast<size_t>(b) * a.n_q * a.hq;
       for (int i = tid; i < a.n_q * a.hq * D; i += kPgThreads) store_out(a.out, row0 * D + i, 0.f, a.out_bf16);
       if (a.lse)
@@ -559,38 +775,42 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
     const uint32_t s0 = p - seg0, s1 = min(p1, seg1) - seg0;
     p = seg0 + s1;
     const int kvh = seg / a.rg, rg = seg % a.rg;
-    const int len = paged_len(a.n_gists, a.own_len, b, a.n_max, a.chunk, a.t_max);
+    const int len = lens[b];
     const int rows = min(R, a.n_q * a.group - rg * R);
     // query row r of the segment -> its row in q and out
     auto out_row = [&](int r) {
       const int x = rg * R + r;
       return (static_cast<size_t>(b) * a.n_q + x / a.group) * a.hq + kvh * a.group + x % a.group;
     };
-    w.load_q(
-        [&](int r) -> const void * {
-          return r < rows ? static_cast<const uint8_t *>(a.q) + out_row(r) * D * (QF32 ? 4 : 2) : nullptr;
-        },
-        a.scale_log2);
-    int64_t lim[NT][2];
+    int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        lim[nt][x] = static_cast<int64_t>(len) - (a.n_q - 1) + (rg * R + 8 * nt + 2 * t + x) / a.group;
+      for (int x = 0; x < 2; ++x) lim[nt][x] = len - (a.n_q - 1) + (rg * R + 8 * nt + 2 * t + x) / a.group;
     const int n = static_cast<int>(s1 - s0);
-    const int64_t first = (static_cast<int64_t>(s0) * kPgWarps + warp) * 16;
+    const int first = (static_cast<int>(s0) * kPgWarps + warp) * 32;
     int mine = 0;  // tiles of this warp that hold a row
-    if (first < len) mine = min(n, static_cast<int>((len - first + kPgStep - 1) / kPgStep));
+    if (first < len) mine = min(n, (len - first + kPgStep - 1) / kPgStep);
     const int32_t *table = a.kv.table + static_cast<size_t>(b) * a.kv.max_pages;
-    auto key0 = [&](int i) { return first + static_cast<int64_t>(i) * kPgStep; };
+    auto key0 = [&](int i) { return first + i * kPgStep; };
     auto raw = [&](int i) {
-      const int64_t k = key0(i) + (lane & 15);
-      return k < len ? k : static_cast<int64_t>(-1);
+      const int k = key0(i) + lane;
+      return k < len ? k : -1;
+    };
+    auto queries = [&] {
+      if (warp < NT)
+        qs.load(
+            warp,
+            [&](int r) -> const void * {
+              return r < rows ? static_cast<const uint8_t *>(a.q) + out_row(r) * D * (QF32 ? 4 : 2) : nullptr;
+            },
+            a.scale_log2);
+      __syncthreads();
     };
     if (a.n_q > 1)
-      w.template run<true>(a.kv, table, kvh, mine, raw, key0, lim, a.status, [] {});
+      w.template run<true>(a.kv, table, kvh, mine, qs, raw, key0, lim, a.status, queries);
     else
-      w.template run<false>(a.kv, table, kvh, mine, raw, key0, lim, a.status, [] {});
+      w.template run<false>(a.kv, table, kvh, mine, qs, raw, key0, lim, a.status, queries);
     __syncthreads();  // every ring is drained: red may overwrite them
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -598,9 +818,9 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
       for (int x = 0; x < 2; ++x) {
         float *dst = red[warp][8 * nt + 2 * t + x];
 #pragma unroll
-        for (int j = 0; j < Warp::KS; ++j)
+        for (int j = 0; j < Warp::MT; ++j)
           *reinterpret_cast<float2 *>(dst + kPartHeader + g * (D / 8) + 2 * j) =
-              make_float2(w.o[nt][j][x], w.o[nt][j][x + 2]);
+              x ? make_float2(w.o[nt][j][0].y, w.o[nt][j][1].y) : make_float2(w.o[nt][j][0].x, w.o[nt][j][1].x);
         if (g == 0) {
           dst[0] = w.m[nt][x];
           dst[1] = w.l[nt][x];
@@ -615,7 +835,7 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
       for (int i = 0; i < kPgWarps; ++i) {
         const float c = exp2_approx(red[i][tid][0] - (M == neg_inf() ? 0.f : M));
         wgt[tid][i] = c;
-        L += c * red[i][tid][1];
+        L = fmaf(c, red[i][tid][1], L);
       }
       rowM[tid] = M;
       rowL[tid] = L;
@@ -624,29 +844,35 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
     const uint32_t c0 = static_cast<uint32_t>(((static_cast<uint64_t>(seg0) + 1) * ctas - 1) / total);
     const uint32_t c1 = static_cast<uint32_t>((static_cast<uint64_t>(seg1) * ctas - 1) / total);
     const bool whole = c0 == c1;
+    auto put = [&](int r, int d, float4 v, float M, float L) {  // 4 dims of a finished row
+      const size_t o = out_row(r) * D + d;
+      const float i = L != 0.f ? 1.f / L : 0.f;
+      if (a.out_bf16) {
+        __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + o);
+        dst[0] = __floats2bfloat162_rn(v.x * i, v.y * i);
+        dst[1] = __floats2bfloat162_rn(v.z * i, v.w * i);
+      } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(v.x * i, v.y * i, v.z * i, v.w * i);
+      }
+      if (d == 0 && a.lse) a.lse[out_row(r)] = L != 0.f ? (M + __log2f(L)) * kLn2 : neg_inf();
+    };
     // this CTA's record: slot 1 if the segment starts in its part, else slot 0
     float *rec = a.part + (static_cast<size_t>(cta) * 2 + (cta == c0 ? 1 : 0)) * R * kRec;
-    for (int i = tid; i < rows * (D / 2); i += kPgThreads) {
-      const int r = i / (D / 2), d = 2 * (i % (D / 2));
-      float x = 0.f, y = 0.f;
+    for (int i = tid; i < rows * (D / 4); i += kPgThreads) {
+      const int r = i / (D / 4), d = 4 * (i % (D / 4));
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kPgWarps; ++k) {
-        const float2 v = *reinterpret_cast<const float2 *>(&red[k][r][kPartHeader + d]);
-        x = fmaf(wgt[r][k], v.x, x);
-        y = fmaf(wgt[r][k], v.y, y);
+        const float4 x = *reinterpret_cast<const float4 *>(&red[k][r][kPartHeader + d]);
+        const float c = wgt[r][k];
+        v = make_float4(fmaf(c, x.x, v.x), fmaf(c, x.y, v.y), fmaf(c, x.z, v.z), fmaf(c, x.w, v.w));
       }
       if (whole) {
-        const float L = rowL[r];
-        const size_t o = out_row(r) * D + d;
-        store_out(a.out, o, L != 0.f ? x / L : 0.f, a.out_bf16);
-        store_out(a.out, o + 1, L != 0.f ? y / L : 0.f, a.out_bf16);
-        if (d == 0 && a.lse) a.lse[out_row(r)] = L != 0.f ? (rowM[r] + __log2f(L)) * kLn2 : neg_inf();
+        put(r, d, v, rowM[r], rowL[r]);
       } else {
-        *reinterpret_cast<float2 *>(rec + static_cast<size_t>(r) * kRec + kPartHeader + d) = make_float2(x, y);
-        if (d == 0) {
-          rec[static_cast<size_t>(r) * kRec] = rowM[r];
-          rec[static_cast<size_t>(r) * kRec + 1] = rowL[r];
-        }
+        float *dst = rec + static_cast<size_t>(r) * kRec;
+        *reinterpret_cast<float4 *>(dst + kPartHeader + d) = v;
+        if (d == 0) *reinterpret_cast<float2 *>(dst) = make_float2(rowM[r], rowL[r]);
       }
     }
     if (!whole) {
@@ -663,33 +889,61 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
       }
       __syncthreads();
       if (last_s) {
-        // records of CTAs c0 .. c1 (c0's in slot 1), in that order
-        auto rec_of = [&](uint32_t c, int r) {
-          return a.part + ((static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * R + r) * kRec;
+        // join the records of CTAs c0 .. c1 (c0's in slot 1), in that order
+        const int nr = static_cast<int>(c1 - c0) + 1;
+        auto rec_of = [&](int k, int r) {
+          return a.part + ((static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * R + r) * kRec;
         };
-        for (int i = tid; i < rows * (D / 2); i += kPgThreads) {
-          const int r = i / (D / 2), d = 2 * (i % (D / 2));
-          float M = neg_inf(), L = 0.f, x = 0.f, y = 0.f;
-          for (uint32_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(rec_of(c, r)));
+        float *cw = reinterpret_cast<float *>(smem);                             // [rows][nr] weights
+        float4 *sums = reinterpret_cast<float4 *>(smem) + (R * kPgMaxCtas) / 4;  // [kPgThreads]
+        for (int r = warp; r < rows; r += kPgWarps) {
+          float M = neg_inf(), L = 0.f;
+          for (int k = lane; k < nr; k += 32) M = fmaxf(M, __ldcg(rec_of(k, r)));
+          M = warp_max(M);
           const float mm = M == neg_inf() ? 0.f : M;
-#pragma unroll 4
-          for (uint32_t c = c0; c <= c1; ++c) {
-            const float *q = rec_of(c, r);
-            const float2 h = __ldcg(reinterpret_cast<const float2 *>(q));
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(q + kPartHeader + d));
-            const float k = exp2_approx(h.x - mm);
-            L = fmaf(k, h.y, L);
-            x = fmaf(k, v.x, x);
-            y = fmaf(k, v.y, y);
+          for (int k = lane; k < nr; k += 32) {
+            const float2 h = __ldcg(reinterpret_cast<const float2 *>(rec_of(k, r)));
+            const float c = exp2_approx(h.x - mm);
+            cw[r * nr + k] = c;
+            L = fmaf(c, h.y, L);
           }
-          const size_t o = out_row(r) * D + d;
-          store_out(a.out, o, L != 0.f ? x / L : 0.f, a.out_bf16);
-          store_out(a.out, o + 1, L != 0.f ? y / L : 0.f, a.out_bf16);
-          if (d == 0 && a.lse) a.lse[out_row(r)] = L != 0.f ? (M + __log2f(L)) * kLn2 : neg_inf();
+          L = warp_sum(L);
+          if (lane == 0) {
+            rowM[r] = M;
+            rowL[r] = L;
+          }
+        }
+        __syncthreads();
+        // items of 4 dims; when they are few, several threads share an item's records
+        const int items = rows * (D / 4);
+        const int share = items >= kPgThreads ? 1 : kPgThreads / items;
+        for (int i0 = 0; i0 < items; i0 += kPgThreads) {
+          const int i = i0 + (share > 1 ? tid % items : tid), part = share > 1 ? tid / items : 0;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int r = i / (D / 4), d = 4 * (i % (D / 4));
+          if (i < items && part < share) {
+#pragma unroll 8
+            for (int k = part; k < nr; k += share) {
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(rec_of(k, r) + kPartHeader + d));
+              const float c = cw[r * nr + k];
+              v = make_float4(fmaf(c, x.x, v.x), fmaf(c, x.y, v.y), fmaf(c, x.z, v.z), fmaf(c, x.w, v.w));
+            }
+          }
+          if (share > 1) {
+            sums[tid] = v;
+            __syncthreads();
+            if (tid < items) {
+              for (int k = 1; k < share; ++k) {
+                const float4 x = sums[tid + k * items];
+                v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+              }
+            }
+          }
+          if (i < items && part == 0) put(r, d, v, rowM[r], rowL[r]);
         }
       }
     }
-    __syncthreads();  // red and the row sums are read: the rings may be used again
+    __syncthreads();  // results, queries and row sums are read: the next segment may overwrite them
   }
   pdl_trigger();
 }
@@ -697,7 +951,7 @@ __global__ void __launch_bounds__(kPgThreads, NT == 1 && !QF32 ? 2 : 1) k_paged_
 // ------------------------------------------------------------------ unfolding
 // Grid (splits, hq, B) as k_unfold: split s of row (b, h) takes its share of
 // the selected chunks; the last split also takes the own chunk.  The rows of
-// the share, in list order, form the 16-row tiles of the warps (a tile may
+// the share, in list order, form the 32-row tiles of the warps (a tile may
 // span chunks and pages); one of the 8 query columns is in use.  The gists
 // of selected chunks (exclude mode) are summed on the CUDA cores while the
 // first copies are in flight, as a record of their own.
@@ -708,9 +962,10 @@ struct PagedUnfoldArgs {
 
 constexpr int kPuWarps = kUnfoldWarps;
 
-template <int D>
+// rings (over them, once drained, the warps' results) | queries | chunk ids | gist logits
+template <int D, int FMT, bool QF32>
 __host__ __device__ inline size_t paged_unfold_smem(int per) {
-  return kPuWarps * PgCfg<D>::kRing + static_cast<size_t>(per) * 8;  // rings | chunk ids | gist logits
+  return kPuWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, 1>) + static_cast<size_t>(per) * 8;
 }
 
 // The CTA's partial (its 2 kPuWarps states in red) goes to the row's split
@@ -777,16 +1032,19 @@ __device__ void paged_unfold_finish(const UnfoldArgs &a, size_t row, int split, 
 }
 
 template <int D, int FMT, bool QF32, bool HILO>
-__global__ void __launch_bounds__(kUnfoldThreads, 4) k_paged_unfold(const __grid_constant__ PagedUnfoldArgs pa) {
+__global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
+    k_paged_unfold(const __grid_constant__ PagedUnfoldArgs pa) {
   using Warp = PgWarp<D, FMT, QF32, HILO, 1>;
+  using Query = typename Warp::Query;
   const UnfoldArgs &a = pa.u;
   const PagedKV &kv = pa.kv;
   extern __shared__ __align__(128) uint8_t smem[];
   const int per = (a.k + a.n_split - 1) / a.n_split;
-  int *items = reinterpret_cast<int *>(smem + kPuWarps * PgCfg<D>::kRing);
+  Query &qs = *reinterpret_cast<Query *>(smem + kPuWarps * PgCfg<D>::kRing);
+  int *items = reinterpret_cast<int *>(smem + kPuWarps * PgCfg<D>::kRing + sizeof(Query));
   float *item_z = reinterpret_cast<float *>(items + per);
+  float(*red)[2 + D] = reinterpret_cast<float(*)[2 + D]>(smem);
   __shared__ int n_items_s, is_last_s, take_s[2];
-  __shared__ float red[2 * kPuWarps][2 + D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   int split, h, b;
   if (a.ready.w) {
@@ -842,23 +1100,25 @@ __global__ void __launch_bounds__(kUnfoldThreads, 4) k_paged_unfold(const __grid
   }
   Warp w;
   w.ring = smem_u32(smem) + warp * PgCfg<D>::kRing;
-  w.load_q(
-      [&](int r) -> const void * {
-        return r == 0 ? static_cast<const uint8_t *>(a.q) + row * D * (QF32 ? 4 : 2) : nullptr;
-      },
-      a.scale_log2);
+  if (warp == 1)
+    qs.load(
+        0,
+        [&](int r) -> const void * {
+          return r == 0 ? static_cast<const uint8_t *>(a.q) + row * D * (QF32 ? 4 : 2) : nullptr;
+        },
+        a.scale_log2);
   __syncthreads();
   const int n_sel = n_items_s, sel_rows = n_sel * a.chunk, n_keys = sel_rows + own;
-  const int n_tiles = (n_keys + 15) >> 4;
+  const int n_tiles = (n_keys + 31) >> 5;
   const int mine = n_tiles > warp ? (n_tiles - warp + kPuWarps - 1) / kPuWarps : 0;
-  auto key0 = [&](int i) { return static_cast<int64_t>((warp + kPuWarps * i) * 16); };
-  auto raw = [&](int i) -> int64_t {
-    const int j = static_cast<int>(key0(i)) + (lane & 15);
+  auto key0 = [&](int i) { return (warp + kPuWarps * i) * 32; };
+  auto raw = [&](int i) {
+    const int j = key0(i) + lane;
     if (j < sel_rows) {
       const int it = kv.chunk.div(j);
-      return static_cast<int64_t>(items[it]) * a.chunk + (j - it * a.chunk);
+      return items[it] * a.chunk + (j - it * a.chunk);
     }
-    return j < n_keys ? static_cast<int64_t>(N) * a.chunk + (j - sel_rows) : static_cast<int64_t>(-1);
+    return j < n_keys ? N * a.chunk + (j - sel_rows) : -1;
   };
   // gists of the selected chunks: D / 32 dims a lane
   constexpr int E = D / 32;
@@ -898,14 +1158,15 @@ __global__ void __launch_bounds__(kUnfoldThreads, 4) k_paged_unfold(const __grid
       for (int e = 0; e < E; ++e) ga[e] = fmaf(p, v[e], ga[e]);
     }
   };
-  w.template run<false>(kv, kv.table + static_cast<size_t>(b) * kv.max_pages, kvh, mine, raw, key0, nullptr, a.status,
-                        gists);
+  w.template run<false>(kv, kv.table + static_cast<size_t>(b) * kv.max_pages, kvh, mine, qs, raw, key0, nullptr,
+                        a.status, gists);
   pdl_trigger();
-  if (t == 0) {  // column 0
+  __syncthreads();  // every ring is drained: red may overwrite them
+  if (t == 0) {     // column 0
 #pragma unroll
-    for (int j = 0; j < Warp::KS; ++j) {
-      red[warp][2 + g * (D / 8) + 2 * j] = w.o[0][j][0];
-      red[warp][2 + g * (D / 8) + 2 * j + 1] = w.o[0][j][2];
+    for (int j = 0; j < Warp::MT; ++j) {
+      red[warp][2 + g * (D / 8) + 2 * j] = w.o[0][j][0].x;
+      red[warp][2 + g * (D / 8) + 2 * j + 1] = w.o[0][j][1].x;
     }
     if (g == 0) {
       red[warp][0] = w.m[0][0];

@@ -66,7 +66,7 @@ gsa_status paged_variant(const gsa_desc *d, const gsa_pdesc *p, Fn fn) {
 
 template <int D, int FMT, bool QF32, bool HILO, int NT>
 gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
-  const size_t smem = paged_attend_smem<D, NT>() + align256((static_cast<size_t>(pa.B) + 1) * 4);
+  const size_t smem = paged_attend_smem<D, FMT, QF32, NT>() + (2 * static_cast<size_t>(pa.B) + 1) * 4;
   const auto kern = k_paged_attend<D, FMT, QF32, HILO, NT>;
   const int grid = std::min(kPgMaxCtas, resident_ctas(kern, kPgThreads, smem));
   return launch(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa);
@@ -107,16 +107,17 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
   ua.lse = lse;
   pa.kv = paged_kv(d, p, k, v, ks, vs, table);
   return paged_variant(d, p, [&](auto dim, auto fmt, auto qf32, auto hilo) {
-    constexpr int D = decltype(dim)::value;
-    const auto kern = k_paged_unfold<D, decltype(fmt)::value, decltype(qf32)::value, decltype(hilo)::value>;
+    constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
+    constexpr bool Q = decltype(qf32)::value;
+    const auto kern = k_paged_unfold<D, F, Q, decltype(hilo)::value>;
     // residency with the largest list share (one split), then the share of the chosen split count; a split is
-    // not made smaller than one 16-row tile a warp
+    // not made smaller than one 32-row tile a warp
     const int k1 = std::max(1, ua.k);
-    const int slots = resident_ctas(kern, kUnfoldThreads, paged_unfold_smem<D>(k1));
-    const int most = std::max(1, static_cast<int>(static_cast<int64_t>(k1) * d->chunk / (16 * kPuWarps)));
+    const int slots = resident_ctas(kern, kUnfoldThreads, paged_unfold_smem<D, F, Q>(k1));
+    const int most = std::max(1, static_cast<int>(static_cast<int64_t>(k1) * d->chunk / (32 * kPuWarps)));
     ua.n_split = one_wave_splits(d->batch * d->hq, slots, std::min(std::min(kUnfoldSplitMax, k1), most));
     return launch(kern, dim3(ua.n_split, d->hq, d->batch), dim3(kUnfoldThreads),
-                  paged_unfold_smem<D>(cdiv(k1, ua.n_split)), stream, pa);
+                  paged_unfold_smem<D, F, Q>(cdiv(k1, ua.n_split)), stream, pa);
   });
 }
 
@@ -245,9 +246,8 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   const Layout L = layout(desc, GSA_OP_PAGED, nullptr);
   if (ws_bytes < L.total) return GSA_ERR_WORKSPACE;
   const int rows = n_q * (desc->hq / desc->hkv);
-  // 8 query rows a segment, or 16 when there are more than 8 and the queries are bf16 (fp32 queries hold twice
-  // the fragments: 16 rows do not fit the registers)
-  const bool wide = rows > 8 && desc->dtype == GSA_BF16;
+  // 8 query rows a segment, or 16 when there are more
+  const bool wide = rows > 8;
   const int rg = cdiv(rows, wide ? 16 : 8);
   if (static_cast<int64_t>(desc->batch) * desc->hkv * rg >= (int64_t(1) << 31) / cdiv(desc->t_max, kPgStep))
     return GSA_ERR_UNSUPPORTED;  // steps are counted in 32 bits
@@ -264,7 +264,7 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   pa.chunk = desc->chunk;
   pa.n_max = desc->n_max;
   pa.t_max = desc->t_max;
-  pa.min_steps = 4;
+  pa.min_steps = 2;
   pa.scale_log2 = resolve_scale(desc) * kLog2e;
   pa.part = reinterpret_cast<float *>(at(ws, L.pg_part));
   pa.counters = reinterpret_cast<uint32_t *>(at(ws, L.pg_seg));
@@ -275,9 +275,7 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   return paged_variant(desc, pdesc, [&](auto dim, auto fmt, auto qf32, auto hilo) {
     constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
     constexpr bool Q = decltype(qf32)::value, H = decltype(hilo)::value;
-    if constexpr (!Q) {
-      if (wide) return launch_paged_attend<D, F, Q, H, 2>(pa, stream);
-    }
+    if (wide) return launch_paged_attend<D, F, Q, H, 2>(pa, stream);
     return launch_paged_attend<D, F, Q, H, 1>(pa, stream);
   });
 }

@@ -86,23 +86,32 @@ def softmax_av(z, v):
     return torch.exp(z - lse) @ v, lse
 
 
-def tolerance(d, reach, vmax, out_bf16, ref, prior=False):
+def logit_error(d, reach, floor):
+    """How far a base-2 logit may be off.
+
+    reach: the largest log2(e) * scale * sum_i |q_i k_i| of an attended row; floor: the same with every |q_i| replaced by
+    the row's largest.  The products of the operands' digits are exact; their fp32 sum over d / 32 matrix instructions a
+    digit (at most 6) may truncate at 2^-22 of the largest partial sum each time, which reach bounds within the digits'
+    own overlap of 2^-3; the query's digits end at 2^-21 of the row's largest element."""
+    return (d / 8 + 5) * 2.0 ** -22 * reach + 2.0 ** -21 * floor
+
+
+def tolerance(dz, vmax, out_bf16, ref, prior=False):
     """How far an output may be from the 64-bit one.
 
-    reach: the largest log2(e) * scale * sum_i |q_i k_i| of an attended row, vmax the largest |value|.  The logit (base
-    2) is a sum of d products in fp32 over d / 16 matrix instructions, twice that with two-term queries; each may
-    truncate its addends and its sum at 2^-22 of the largest partial sum, which `reach` bounds, so it is off by at most
-    (d / 8 + 4) 2^-22 reach; a query rounds at 2^-22 when fp32 (two fp16 terms), adding 2^-22 reach.  With ln 2 < 1 that
-    bounds the relative error of each weight; base-2 exponential, two-term weights, scales and fp32 sums add less than
-    2^-19.  A weighted mean of values moves by at most twice the weights' relative error times vmax.  bf16 outputs:
-    one-term weights add 2^-11, the output's rounding 2^-8 of its value.  prior: the scoring pass sums the gists' values
-    with weights of two bf16 terms, 2^-16."""
-    rel = (d / 8 + 5) * 2.0 ** -22 * reach + 2.0 ** -19 + (2.0 ** -16 if prior else 0.0)
+    With ln 2 < 1, dz (logit_error) bounds the relative error of each weight; base-2 exponential, scales and fp32 sums
+    add less than 2^-19.  A weighted mean of values moves by at most twice the weights' relative error times vmax, the
+    largest |value|.  The weights' digits enter only the sum of values: int8 ends at half of 2^-21 (fp32 outputs) or
+    2^-14 (bf16) of the largest weight of 32 keys, so a tile is off by at most 32 2^-22 (2^-15) of a weight that the
+    normaliser holds, 2^-17 (2^-10) vmax together; e4m3's digits are below that (2^-22 or 2^-12 relative, 32 2^-30 or
+    32 2^-18 of the largest).  bf16 outputs round at 2^-8.  prior: the scoring pass sums the gists' values with
+    weights of two bf16 terms, 2^-16."""
+    rel = dz + 2.0 ** -19 + (2.0 ** -16 if prior else 0.0)
     if not out_bf16:
-        return 2 * rel * vmax
-    return 2 * (rel + 2.0 ** -11) * vmax + 2.0 ** -8 * ref.abs()
+        return 2 * rel * vmax + 2.0 ** -17 * vmax
+    return 2 * rel * vmax + 2.0 ** -10 * vmax + 2.0 ** -8 * ref.abs()
 
 
-def lse_tolerance(d, reach, lse):
-    """The logits' error (see tolerance) times ln 2, and the rounding of ln and of the result."""
-    return (d / 8 + 5) * 2.0 ** -22 * reach + 2.0 ** -19 + 2.0 ** -21 * abs(lse)
+def lse_tolerance(dz, lse):
+    """The logits' error, and the rounding of ln and of the result."""
+    return dz + 2.0 ** -19 + 2.0 ** -21 * abs(lse)

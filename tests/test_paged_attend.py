@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from _paged import Cache, lse_tolerance, softmax_av, tolerance
+from _paged import Cache, logit_error, lse_tolerance, softmax_av, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -39,20 +39,23 @@ def descs(c, hq, *, dtype="bf16", out="f32", topk=0, n_max=1, exclude=True, scal
 def check_row(got, got_lse, q, k, v, z_extra, v_extra, scale, d, out_bf16, what, prior=False):
     """One output row against exact attention of q over rows k, v and the given extra logits and values."""
     z = (k @ q) * scale
-    reach = float((k.abs() @ q.abs()).max()) * scale * LOG2E if len(k) else 0.0
+    dz = 0.0
+    if len(k):
+        reach = float((k.abs() @ q.abs()).max()) * scale * LOG2E
+        dz = logit_error(d, reach, float(q.abs().max() * k.abs().sum(-1).max()) * scale * LOG2E)
     vv = v
     if z_extra is not None:
         z, vv = torch.cat([z, z_extra]), torch.cat([v, v_extra])
     ref, lse = softmax_av(z, vv)
     vmax = float(vv.abs().max()) if len(vv) else 0.0
     err = (got.double() - ref).abs()
-    lim = tolerance(d, reach, vmax, out_bf16, ref, prior)
+    lim = tolerance(dz, vmax, out_bf16, ref, prior)
     allowed = float(torch.as_tensor(lim).max())
     assert bool((err <= lim).all()), f"{what}: off by {float(err.max()):.3e}, allowed {allowed:.3e}"
     if math.isinf(float(lse)):
         assert float(got_lse) == float(lse), f"{what}: lse {float(got_lse)}"
     else:
-        assert abs(float(got_lse) - float(lse)) <= lse_tolerance(d, reach, float(lse)), f"{what}: lse"
+        assert abs(float(got_lse) - float(lse)) <= lse_tolerance(dz, float(lse)), f"{what}: lse"
 
 
 def run_attend(c, hq, n_q, *, dtype="bf16", out="f32", seed=1, scale=0.0, n_gists=None, own_len=None, q_std=1.0):
