@@ -8,27 +8,26 @@
 // The product kernel of both readers (k_paged_attend: all rows of a
 // sequence; k_paged_unfold: selected chunks and the own chunk of one query
 // head) is one warp working through tiles of 32 rows:
-//   z = K q        S^T[16 keys x 8 queries], mma.sync m16n8k32 on the codes as
-//                  they are, the KEYS as the A operand: a kv head's 4..8 query
-//                  heads fill the 8 columns, where queries as A would leave
-//                  8..12 of 16 rows idle;
+//   z = K q        S^T[16 keys x 8 queries] with mma.sync, the KEYS as the A
+//                  operand: a kv head's 4..8 query heads fill the 8 columns,
+//                  where queries as A would leave 8..12 of 16 rows idle;
 //   p = 2^(z - m)  lazy online softmax in fp32 (m raised when exceeded by
-//                  kPgSlack), the scale of K applied to z, that of V to p;
-//   O^T += V^T p   m16n8k32 with V^T as A (4 x 4 byte transposes of the codes
-//                  in registers) and p as B (movmatrix turns the accumulator
-//                  layout of S^T into it).
-// The 8-bit operands of the other side are written as sums of 8-bit digits,
-// one product each, so the codes need no conversion:
-//   e4m3 (4 significant bits a digit): a bf16 query is 2 digits, the second
-//     in an accumulator of its own at 2^4 times the scale; an fp32 one 3 + 3 at
-//     2^12.  A row is scaled by a power of two so that its largest element
-//     lies in [128, 256): digits end at 2^-10, 2^-22 (2^-30) of it.
-//   int8 (7 bits a digit, fixed point): 3 digits for bf16 queries (2^-20 of the
-//     row's largest element), 4 for fp32 (2^-28); sums are exact integers.
-//   p times the scale of V is scaled by the largest of the tile's 32 in its
-//     column: e4m3 3 digits (2^-12 of the weight, 2^-18 of the largest) or 6
-//     (2^-22, 2^-30), int8 2 digits (2^-15 of the largest) or 3 (2^-22): the
-//     fewer for bf16 outputs, whose own rounding is 2^-8.
+//                  kPgSlack), the scale of K applied to z, that of V to p
+//                  relative to the tile's largest;
+//   O^T += V^T p   V^T as A (the codes interleaved in registers) and p as B
+//                  (movmatrix turns the accumulator layout of S^T into it).
+// Operands: codes are exact in fp16 and in int8, and no query or weight is
+// rounded to fewer bits than the result keeps.
+//   int8 keys: m16n8k32 on the codes as they are; a query is 3 digits of 7 bits
+//     (bf16; 2^-20 of the row's largest element) or 4 (fp32; 2^-27), one product
+//     each; sums are exact integers.
+//   e4m3 keys: m16n8k16 on fp16 (on sm_100a the e4m3 form of mma.sync runs as
+//     conversions and two fp16 products, so the codes are converted once here);
+//     queries as one fp16 term after a power-of-two scaling of the row to
+//     [2^14, 2^15) (exact for bf16 down to 2^-38 of the largest), fp32 ones as
+//     two (22 bits).
+//   weights: fp16 after scaling by 2^11; one term for bf16 outputs (2^-12
+//     against the 2^-8 of the output's rounding), two for fp32 (2^-22).
 // Statistics, sums of weights and the running output are fp32.
 //
 // What bounds it: HBM reads of the codes.  Every warp copies its tiles with
@@ -68,7 +67,8 @@ struct PagedKV {
   FastDiv page, chunk;
 };
 
-constexpr float kPgSlack = 16.0f;  // p <= 2^16 before the reference is raised (p is fp32)
+constexpr float kPgSlack = 4.0f;     // p <= 2^4 before the reference is raised
+constexpr float kPgPScale = 2048.f;  // p is scaled by 2^11 into fp16's range (<= 2^15)
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -79,18 +79,34 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// c += A B on 8-bit codes (16 x 32 times 32 x 8).
-__device__ __forceinline__ void mma_16832(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+// c = A B (FIRST) or c += A B: fp16 16 x 16 times 16 x 8, int8 16 x 32 times 32 x 8.
+template <bool FIRST>
+__device__ __forceinline__ void mma_f16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  if (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_16832(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+template <bool FIRST>
+__device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  if (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 8x8 block of 16-bit elements transposed across the warp's accumulator layout.
@@ -98,13 +114,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// The larger, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
 }
 
 // (a.x * b.x + c.x, a.y * b.y + c.y)
@@ -117,31 +126,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return *reinterpret_cast<const float2 *>(&r);
 }
 
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
 __device__ __forceinline__ float2 unpack_h2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
-// e4m3 pair (16 bits) of an fp16 pair, and back.
-__device__ __forceinline__ uint16_t h2_to_e4(__half2 x) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
-  return r;
-}
-__device__ __forceinline__ __half2 e4_to_h2(uint16_t x) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
-  return *reinterpret_cast<const __half2 *>(&r);
-}
-
-// N e4m3 digits of an fp16 pair: out[i] is the rounding of what out[0..i-1] left.  Returns the remainder (exact).
-template <int N>
-__device__ __forceinline__ __half2 e4_digits(__half2 x, uint16_t *out) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    out[i] = h2_to_e4(x);
-    x = __hsub2(x, e4_to_h2(out[i]));
-  }
-  return x;
 }
 
 // Four codes -> two fp16 pairs (bytes 0,1 and bytes 2,3), exact.
@@ -157,9 +147,10 @@ __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t &lo, uint32_t &
     lo = *reinterpret_cast<const uint32_t *>(&x);
     hi = *reinterpret_cast<const uint32_t *>(&y);
   } else {
-    const __half2 x = e4_to_h2(static_cast<uint16_t>(w)), y = e4_to_h2(static_cast<uint16_t>(w >> 16));
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 
@@ -184,26 +175,18 @@ __device__ __forceinline__ uint32_t v_off(uint32_t r, uint32_t p) {
   return (r ^ ((r >> 2) & 1)) * 64 + ((p ^ (((r >> 1) & 1) << 1)) << 4);
 }
 
-// Digits of the queries: how many, and how they group into two accumulators
-// (the value is acc[0] + acc[1] * kRest for e4m3, acc[0] * kTop + acc[1] for
-// int8, whose first digits come first).
-template <int FMT, bool QF32>
-struct QDigits {
-  static constexpr int kFirst = FMT == kFmtI8 ? 2 : (QF32 ? 3 : 1);  // digits of acc[0]
-  static constexpr int kN = FMT == kFmtI8 ? (QF32 ? 4 : 3) : 2 * kFirst;
-  static constexpr float kUp = QF32 ? 4096.f : 16.f;   // e4m3: scale of the second group
-  static constexpr int kBits = 7 * kN - 1;             // int8: |fixed point| < 2^kBits
-  static constexpr float kTop = kN == 4 ? 16384.f : 128.f;
-};
-
-// The queries of a segment in shared memory, as the B fragments of their
-// digits: [NT][digit][k-step of 32 dims][lane], and the factor of each row's
-// logits.  Row n (< 8 NT) is row(n), null when unused.
+// The queries of a segment in shared memory, as B fragments:
+// [NT][term][k-step][lane], and the factor of each row's logits.  Row n
+// (< 8 NT) is row(n), null when unused.
+//   e4m3: kN fp16 terms, k-steps of 16 dims;
+//   int8: kN digits of a fixed-point number |v| < 2^kBits, k-steps of 32 dims.
 template <int D, int FMT, bool QF32, int NT>
 struct PgQuery {
-  using Dg = QDigits<FMT, QF32>;
-  static constexpr int KS = D / 32;
-  uint2 frag[NT][Dg::kN][KS][32];
+  static constexpr bool kI8 = FMT == kFmtI8;
+  static constexpr int kN = kI8 ? (QF32 ? 4 : 3) : (QF32 ? 2 : 1);
+  static constexpr int KS = kI8 ? D / 32 : D / 16;
+  static constexpr int kTopExp = kI8 ? 7 * kN - 1 : 15;  // the row's largest is brought into [2^(kTopExp-1), 2^kTopExp)
+  uint2 frag[NT][kN][KS][32];
   float f[8 * NT];
 
   // Group nt, by one warp.
@@ -230,9 +213,7 @@ struct PgQuery {
     for (int i = 0; i < D / 4; ++i) a = max(a, __float_as_uint(x[i]) & 0x7fffffffu);
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    // power of two that brings the row's maximum into [2^(top-1), 2^top); none for a row of zeros.  An inf or NaN
-    // makes the row's logits NaN.
-    constexpr int kTopExp = FMT == kFmtI8 ? Dg::kBits : 8;
+    // a power of two; none for a row of zeros.  An inf or NaN makes the row's logits NaN.
     int sh = 0;
     if (a != 0 && a < 0x7f800000u) sh = min(kTopExp - 1 - (static_cast<int>(a >> 23) - 127), 120);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
@@ -240,43 +221,35 @@ struct PgQuery {
     if (t == 0) f[8 * nt + g] = a < 0x7f800000u ? down : __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      // words of b0 (dims 8 s' + 0..3) and b1 (+ 4..7) of this k-step
-      uint32_t w[Dg::kN][2];
+      uint32_t w[kN][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float *y = x + 8 * s + 4 * h;
-        if (FMT == kFmtI8) {
-          uint32_t d[Dg::kN][4];
+        if (kI8) {  // word h: dims 8 s + 4 h + 0..3
+          const float *y = x + 8 * s + 4 * h;
+          uint32_t d[kN][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             int v = __float2int_rn(y[i] * up);
 #pragma unroll
-            for (int k = Dg::kN - 1; k >= 0; --k) {  // last digit first; each in [-64, 63], the first takes the rest
+            for (int k = kN - 1; k >= 0; --k) {  // the last digit first; each in [-64, 63], the first takes the rest
               const int top = k == 0 ? v : ((v + 64) & 127) - 64;
               d[k][i] = static_cast<uint32_t>(top) & 0xffu;
               v = (v - top) >> 7;
             }
           }
 #pragma unroll
-          for (int k = 0; k < Dg::kN; ++k) w[k][h] = d[k][0] | d[k][1] << 8 | d[k][2] << 16 | d[k][3] << 24;
-        } else {
-          uint16_t d[2][Dg::kN];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float u = y[2 * i] * up, v = y[2 * i + 1] * up;
-            const __half2 r = __floats2half2_rn(u, v);  // exact for bf16 down to fp16's subnormals
-            const float2 rf = __half22float2(r);
-            const float2 left = __half22float2(e4_digits<Dg::kFirst>(r, d[i]));
-            e4_digits<Dg::kN - Dg::kFirst>(
-                __floats2half2_rn(((u - rf.x) + left.x) * Dg::kUp, ((v - rf.y) + left.y) * Dg::kUp),
-                d[i] + Dg::kFirst);
+          for (int k = 0; k < kN; ++k) w[k][h] = d[k][0] | d[k][1] << 8 | d[k][2] << 16 | d[k][3] << 24;
+        } else {  // word h: dims 4 s + 2 h + 0, 1
+          const float u = x[(4 * s + 2 * h) % (D / 4)] * up, v = x[(4 * s + 2 * h + 1) % (D / 4)] * up;
+          w[0][h] = pack_h2(u, v);
+          if (QF32) {
+            const float2 r = unpack_h2(w[0][h]);
+            w[kN - 1][h] = pack_h2(u - r.x, v - r.y);
           }
-#pragma unroll
-          for (int k = 0; k < Dg::kN; ++k) w[k][h] = d[0][k] | static_cast<uint32_t>(d[1][k]) << 16;
         }
       }
 #pragma unroll
-      for (int k = 0; k < Dg::kN; ++k) frag[nt][k][s][lane] = make_uint2(w[k][0], w[k][1]);
+      for (int k = 0; k < kN; ++k) frag[nt][k][s][lane] = make_uint2(w[k][0], w[k][1]);
     }
   }
 };
@@ -286,13 +259,9 @@ template <int D, int FMT, bool QF32, bool HILO, int NT>
 struct PgWarp {
   using Cfg = PgCfg<D>;
   using Query = PgQuery<D, FMT, QF32, NT>;
-  using Dg = QDigits<FMT, QF32>;
-  using Acc = typename std::conditional<FMT == kFmtI8, int, float>::type;
   static constexpr int S = Cfg::kStages;
-  static constexpr int MT = D / 16;  // m-tiles of O^T
-  // digits of a weight; int8: the first two share an accumulator
-  static constexpr int PN = FMT == kFmtI8 ? (HILO ? 3 : 2) : (HILO ? 6 : 3);
-  static constexpr float kPTop = FMT == kFmtI8 ? (HILO ? 2080768.f : 16256.f) : 448.f;  // 127 * 2^7 or 2^14
+  static constexpr int MT = D / 16;           // m-tiles of O^T
+  static constexpr int PN = HILO ? 2 : 1;     // fp16 terms of a weight
 
   float m[NT][2], l[NT][2];  // columns 2t, 2t + 1
   float2 o[NT][MT][2];       // O^T: dims g*D/8 + 2j and + 2j + 1, (column 2t, column 2t + 1)
@@ -380,165 +349,114 @@ struct PgWarp {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(base + Cfg::kMask));
     // ---- z: value e of half h: key 16 h + g + 8 (e >> 1), column 2 t + (e & 1)
     float z[2][NT][4];
-    {
-      Acc acc[2][NT][2][4];
+    logits(qs, base, z);
+    bool masked = mask != 0xffffffffu;  // some key is not there, or not for every column
+    if (CAUSAL) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) masked = masked || key0 + 32 > lim[nt][0] || key0 + 32 > lim[nt][1];
+      masked = __any_sync(0xffffffffu, masked);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float kg[2] = {ldsf(scb + 64 * h), ldsf(scb + 64 * h + 32)};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 f = *reinterpret_cast<const float2 *>(&qs.f[8 * nt + 2 * t]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[h][nt][e] *= kg[e >> 1] * (e & 1 ? f.y : f.x);
+      }
+    }
+    if (masked) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[h][nt][k][e] = 0;
-      uint32_t kw[D / 64][4][4];  // [piece][row g + 8 i][word]
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds4(base + ((i * (D / 64) + c) * 32 + lane) * 16, kw[c][i]);
-#pragma unroll
-      for (int k = 0; k < Dg::kN; ++k) {
-        const int group = k < Dg::kFirst ? 0 : 1;
-        if (FMT == kFmtI8 && k == (group ? Dg::kFirst + 1 : 1)) {  // second digit of its accumulator
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[h][nt][group][e] *= 128;
-        }
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 b = qs.frag[nt][k][s][lane];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              mma_16832(acc[h][nt][group], kw[s / 2][2 * h][2 * (s & 1)], kw[s / 2][2 * h + 1][2 * (s & 1)],
-                        kw[s / 2][2 * h][2 * (s & 1) + 1], kw[s / 2][2 * h + 1][2 * (s & 1) + 1], b);
-          }
-      }
-      bool over = false;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float kg[2] = {ldsf(scb + 64 * h), ldsf(scb + 64 * h + 32)};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float2 f = *reinterpret_cast<const float2 *>(&qs.f[8 * nt + 2 * t]);
-#pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float v = FMT == kFmtI8 ? fmaf(static_cast<float>(acc[h][nt][0][e]), Dg::kTop,
-                                                 static_cast<float>(acc[h][nt][1][e]))
-                                          : fmaf(static_cast<float>(acc[h][nt][1][e]), 1.f / Dg::kUp,
-                                                 static_cast<float>(acc[h][nt][0][e]));
             const int key = 16 * h + g + 8 * (e >> 1);
-            bool see = (mask >> key) & 1u;
-            if (CAUSAL) see = see && key0 + key < lim[nt][e & 1];
-            z[h][nt][e] = see ? v * (kg[e >> 1] * (e & 1 ? f.y : f.x)) : neg_inf();
-            over = over || z[h][nt][e] > m[nt][e & 1] + kPgSlack;
+            if (!((mask >> key) & 1u) || (CAUSAL && key0 + key >= lim[nt][e & 1])) z[h][nt][e] = neg_inf();
           }
-        }
+    }
+    bool over = false;
+    float mx[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mx[nt][x] = fmaxf(fmaxf(z[0][nt][x], z[0][nt][x + 2]), fmaxf(z[1][nt][x], z[1][nt][x + 2]));
+        over = over || mx[nt][x] > m[nt][x] + kPgSlack;
       }
-      if (__any_sync(0xffffffffu, over)) {  // raise the references, rescale
+    if (__any_sync(0xffffffffu, over)) {  // raise the references, rescale
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float c[2];
+      for (int nt = 0; nt < NT; ++nt) {
+        float c[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float mx = fmaxf(fmaxf(z[0][nt][x], z[0][nt][x + 2]), fmaxf(z[1][nt][x], z[1][nt][x + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            c[x] = mx > m[nt][x] ? exp2_approx(m[nt][x] - mx) : 1.f;  // 0 when there was no reference
-            l[nt][x] *= c[x];
-            m[nt][x] = fmaxf(m[nt][x], mx);
-          }
-#pragma unroll
-          for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              o[nt][j][y].x *= c[0];
-              o[nt][j][y].y *= c[1];
-            }
+        for (int x = 0; x < 2; ++x) {
+          float v = mx[nt][x];
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          c[x] = v > m[nt][x] ? exp2_approx(m[nt][x] - v) : 1.f;  // 0 when there was no reference
+          l[nt][x] *= c[x];
+          m[nt][x] = fmaxf(m[nt][x], v);
         }
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            o[nt][j][y].x *= c[0];
+            o[nt][j][y].y *= c[1];
+          }
       }
     }
-    // ---- weights: p, times the scale of V, relative to the column's largest of the tile; their digits as B fragments
-    uint2 pb[PN][NT];
-    float2 back[NT];
+    // ---- weights: p times the scale of V relative to the tile's largest (scales are >= 0, so their bits order like
+    // the values; fmaxf drops a NaN scale here, which then reaches only the columns that see its keys)
     float vg[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) vg[i] = ldsf(scb + 128 + 32 * i);
+    const float vmax = __uint_as_float(__reduce_max_sync(
+        0xffffffffu, __float_as_uint(fmaxf(fmaxf(fmaxf(vg[0], vg[1]), fmaxf(vg[2], vg[3])), 0.f))));
+    const float inv = vmax != 0.f ? __fdividef(kPgPScale, vmax) : 0.f;
+    const float back = vmax * (1.f / kPgPScale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vg[i] *= inv;
+    uint32_t pb[PN][NT][2][2];  // [term][group][half]: B fragments, keys 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float w[2][4], top[2];
       const float m0 = m[nt][0] == neg_inf() ? 0.f : m[nt][0], m1 = m[nt][1] == neg_inf() ? 0.f : m[nt][1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float p = exp2_approx(z[h][nt][e] - (e & 1 ? m1 : m0));
           l[nt][e & 1] += p;
-          w[h][e] = z[h][nt][e] == neg_inf() ? 0.f : p * vg[2 * h + (e >> 1)];  // (a scale of NaN stays with its keys)
+          w[e] = p * vg[2 * h + (e >> 1)];
+        }
+        if (CAUSAL && masked) {  // a NaN scale stays with the columns that see its keys
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (z[h][nt][e] == neg_inf()) w[e] = 0.f;
         }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float a = max_nan(max_nan(w[0][x], w[0][x + 2]), max_nan(w[1][x], w[1][x + 2]));
-        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 4));
-        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 8));
-        top[x] = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 16));
-      }
-      // (weights whose reciprocal fp32 does not hold, below kPTop 2^-126, are zero)
-      const float i0 = top[0] > kPTop * 1.18e-38f ? __fdividef(kPTop, top[0]) : 0.f;
-      const float i1 = top[1] > kPTop * 1.18e-38f ? __fdividef(kPTop, top[1]) : 0.f;
-      back[nt] = make_float2(top[0] * (1.f / kPTop), top[1] * (1.f / kPTop));
-      // 16-bit element (key g, column): digits of keys g and g + 8 of the half
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t dig[PN];
-        if (FMT == kFmtI8) {
-          int v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = __float2int_rn(w[h][e] * (e & 1 ? i1 : i0));
-#pragma unroll
-          for (int k = PN - 1; k >= 0; --k) {
-            // bytes: column 2t (keys g, g + 8), column 2t + 1 (keys g, g + 8); the last digit in [-64, 63]
-            int r[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              r[e] = k == 0 ? v[e] : v[e] + 64;
-              v[e] = r[e] >> 7;
-              if (k > 0) r[e] = (r[e] & 127) - 64;
-            }
-            dig[k] = __byte_perm(__byte_perm(r[0], r[2], 0x0040), __byte_perm(r[1], r[3], 0x0040), 0x5410);
-          }
-        } else {
-          uint16_t d0[PN], d1[PN];
-          const float a0 = w[h][0] * i0, a2 = w[h][2] * i0, b0 = w[h][1] * i1, b2 = w[h][3] * i1;
-          const __half2 ha = __floats2half2_rn(a0, a2), hb = __floats2half2_rn(b0, b2);
-          const __half2 ra = e4_digits<3>(ha, d0), rb = e4_digits<3>(hb, d1);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t hi = pack_h2(w[2 * i], w[2 * i + 1]);
+          pb[0][nt][h][i] = movmatrix_trans(hi);
           if (HILO) {
-            const float2 fa = __half22float2(ha), fb = __half22float2(hb);
-            const float2 la = __half22float2(ra), lb = __half22float2(rb);
-            e4_digits<3>(__floats2half2_rn(((a0 - fa.x) + la.x) * 4096.f, ((a2 - fa.y) + la.y) * 4096.f),
-                         d0 + (HILO ? 3 : 0));
-            e4_digits<3>(__floats2half2_rn(((b0 - fb.x) + lb.x) * 4096.f, ((b2 - fb.y) + lb.y) * 4096.f),
-                         d1 + (HILO ? 3 : 0));
+            const float2 r = unpack_h2(hi);
+            pb[PN - 1][nt][h][i] = movmatrix_trans(pack_h2(w[2 * i] - r.x, w[2 * i + 1] - r.y));
           }
-#pragma unroll
-          for (int k = 0; k < PN; ++k) dig[k] = d0[k] | static_cast<uint32_t>(d1[k]) << 16;
         }
-#pragma unroll
-        for (int k = 0; k < PN; ++k) (h ? pb[k][nt].y : pb[k][nt].x) = movmatrix_trans(dig[k]);
       }
     }
-    // ---- O^T += V^T p: dims in words of 4 codes, rows 2t, 2t+8, 2t+1, 2t+9 of each half
+    // ---- O^T += V^T p: dims in words of 4 codes, rows 2t, 2t + 1, 2t + 8, 2t + 9 of each half
     constexpr int kW = D / 32;
     uint32_t vr[2][4][kW];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t r = 16 * h + 2 * t + (i >> 1) + 8 * (i & 1);
+        const uint32_t r = 16 * h + 2 * t + (i & 1) + 8 * (i >> 1);
         if constexpr (D == 128) {
           lds4(base + Cfg::kK + v_off<D>(r, g), vr[h][i]);
         } else {
@@ -547,50 +465,102 @@ struct PgWarp {
                        : "r"(base + Cfg::kK + v_off<D>(r, g >> 1) + (g & 1) * 8));
         }
       }
+    const float2 back2 = make_float2(back, back);
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      uint32_t a[2][4];  // [half][dim]: four keys' codes
+    for (int w = 0; w < kW; ++w)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t x = __byte_perm(vr[h][0][w], vr[h][1][w], 0x5140);
-        const uint32_t y = __byte_perm(vr[h][0][w], vr[h][1][w], 0x7362);
-        const uint32_t u = __byte_perm(vr[h][2][w], vr[h][3][w], 0x5140);
-        const uint32_t v = __byte_perm(vr[h][2][w], vr[h][3][w], 0x7362);
-        a[h][0] = __byte_perm(x, u, 0x5410);
-        a[h][1] = __byte_perm(x, u, 0x7632);
-        a[h][2] = __byte_perm(y, v, 0x5410);
-        a[h][3] = __byte_perm(y, v, 0x7632);
-      }
+      for (int j = 0; j < 2; ++j) {  // dims 4 w + 2 j and + 1 of the lane's D / 8
+        float d[NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a0, a1, a2, a3;  // (row 2t, row 2t + 1) pairs of the two dims, then rows 2t + 8, 2t + 9
+          codes_to_h2<FMT>(__byte_perm(vr[h][0][w], vr[h][1][w], j ? 0x7362 : 0x5140), a0, a1);
+          codes_to_h2<FMT>(__byte_perm(vr[h][2][w], vr[h][3][w], j ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (h == 0)
+              mma_f16<true>(d[nt], a0, a1, a2, a3, pb[0][nt][h][0], pb[0][nt][h][1]);
+            else
+              mma_f16<false>(d[nt], a0, a1, a2, a3, pb[0][nt][h][0], pb[0][nt][h][1]);
+            if (HILO) mma_f16<false>(d[nt], a0, a1, a2, a3, pb[PN - 1][nt][h][0], pb[PN - 1][nt][h][1]);
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          constexpr int kAcc = HILO ? 2 : 1;
-          Acc d[kAcc][4];
-#pragma unroll
-          for (int k = 0; k < kAcc; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[k][e] = 0;
-#pragma unroll
-          for (int k = 0; k < PN; ++k) {
-            const int group = FMT == kFmtI8 ? k / 2 : k / 3;
-            if (FMT == kFmtI8 && k == 1) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) d[0][e] *= 128;
-            }
-            mma_16832(d[group], a[0][2 * j], a[0][2 * j + 1], a[1][2 * j], a[1][2 * j + 1], pb[k][nt]);
-          }
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = static_cast<float>(d[0][e]);
-            if (HILO)
-              v[e] = FMT == kFmtI8 ? fmaf(v[e], 128.f, static_cast<float>(d[kAcc - 1][e]))
-                                   : fmaf(static_cast<float>(d[kAcc - 1][e]), 1.f / 4096.f, v[e]);
-          }
-          o[nt][2 * w + j][0] = fma2(back[nt], make_float2(v[0], v[1]), o[nt][2 * w + j][0]);
-          o[nt][2 * w + j][1] = fma2(back[nt], make_float2(v[2], v[3]), o[nt][2 * w + j][1]);
+          o[nt][2 * w + j][0] = fma2(back2, make_float2(d[nt][0], d[nt][1]), o[nt][2 * w + j][0]);
+          o[nt][2 * w + j][1] = fma2(back2, make_float2(d[nt][2], d[nt][3]), o[nt][2 * w + j][1]);
         }
+      }
+  }
+
+  // z[half][group][e] = codes . query terms (without the scales).
+  __device__ __forceinline__ void logits(const Query &qs, uint32_t base, float (*z)[NT][4]) {
+    const int lane = threadIdx.x & 31;
+    uint32_t kw[D / 64][4][4];  // [piece][row g + 8 i][word]
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds4(base + ((i * (D / 64) + c) * 32 + lane) * 16, kw[c][i]);
+    if constexpr (FMT == kFmtI8) {
+      // digits 0, 1 share an accumulator (times 128 in between), so do 2, 3
+      int acc[2][2][NT][4];
+#pragma unroll
+      for (int k = 0; k < Query::kN; ++k) {
+        if (k & 1)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[k / 2][h][nt][e] *= 128;
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = qs.frag[nt][k][s][lane];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = kw[s / 2][2 * h][2 * (s & 1)], a1 = kw[s / 2][2 * h + 1][2 * (s & 1)];
+              const uint32_t a2 = kw[s / 2][2 * h][2 * (s & 1) + 1], a3 = kw[s / 2][2 * h + 1][2 * (s & 1) + 1];
+              if (s == 0 && !(k & 1))
+                mma_s8<true>(acc[k / 2][h][nt], a0, a1, a2, a3, b.x, b.y);
+              else
+                mma_s8<false>(acc[k / 2][h][nt], a0, a1, a2, a3, b.x, b.y);
+            }
+          }
+      }
+      // three digits: (d0 128 + d1) 128 + d2; four: (d0 128 + d1) 2^14 + (d2 128 + d3)
+      constexpr float kTop = Query::kN == 4 ? 16384.f : 128.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            z[h][nt][e] = fmaf(static_cast<float>(acc[0][h][nt][e]), kTop, static_cast<float>(acc[1][h][nt][e]));
+    } else {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          codes_to_h2<FMT>(kw[s / 4][2 * h][s & 3], a[h][0], a[h][2]);
+          codes_to_h2<FMT>(kw[s / 4][2 * h + 1][s & 3], a[h][1], a[h][3]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < Query::kN; ++k) {
+            const uint2 b = qs.frag[nt][k][s][lane];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (s == 0 && k == 0)
+                mma_f16<true>(z[h][nt], a[h][0], a[h][1], a[h][2], a[h][3], b.x, b.y);
+              else
+                mma_f16<false>(z[h][nt], a[h][0], a[h][1], a[h][2], a[h][3], b.x, b.y);
+            }
+          }
+      }
     }
   }
 
@@ -734,8 +704,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
   using Warp = PgWarp<D, FMT, QF32, HILO, NT>;
   using Query = typename Warp::Query;
   constexpr int R = 8 * NT, kRec = D + kPartHeader;
-  static_assert(kPgWarps * PgCfg<D>::kRing >= (kPgWarps * R * kRec + 4 * kPgThreads) * 4, "results fit over the rings");
-  static_assert(kPgWarps * PgCfg<D>::kRing >= (R * kPgMaxCtas + 4 * kPgThreads) * 4, "a join fits over the rings");
+  static_assert(PgCfg<D>::kRing >= R * kRec * 4, "the warps' results fit over the rings");
   extern __shared__ __align__(128) uint8_t smem[];
   Query &qs = *reinterpret_cast<Query *>(smem + kPgWarps * PgCfg<D>::kRing);
   uint32_t *pre = reinterpret_cast<uint32_t *>(smem + paged_attend_smem<D, FMT, QF32, NT>());
@@ -889,57 +858,59 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
       }
       __syncthreads();
       if (last_s) {
-        // join the records of CTAs c0 .. c1 (c0's in slot 1), in that order
+        // join the records of CTAs c0 .. c1 (c0's in slot 1), in that order: all of them (or as many as the rings
+        // hold) are copied to shared memory at once, then summed
         const int nr = static_cast<int>(c1 - c0) + 1;
-        auto rec_of = [&](int k, int r) {
-          return a.part + ((static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * R + r) * kRec;
-        };
-        float *cw = reinterpret_cast<float *>(smem);                             // [rows][nr] weights
-        float4 *sums = reinterpret_cast<float4 *>(smem) + (R * kPgMaxCtas) / 4;  // [kPgThreads]
-        for (int r = warp; r < rows; r += kPgWarps) {
-          float M = neg_inf(), L = 0.f;
-          for (int k = lane; k < nr; k += 32) M = fmaxf(M, __ldcg(rec_of(k, r)));
-          M = warp_max(M);
-          const float mm = M == neg_inf() ? 0.f : M;
-          for (int k = lane; k < nr; k += 32) {
-            const float2 h = __ldcg(reinterpret_cast<const float2 *>(rec_of(k, r)));
-            const float c = exp2_approx(h.x - mm);
-            cw[r * nr + k] = c;
-            L = fmaf(c, h.y, L);
-          }
-          L = warp_sum(L);
-          if (lane == 0) {
-            rowM[r] = M;
-            rowL[r] = L;
-          }
+        constexpr int kFit = kPgWarps * PgCfg<D>::kRing / (R * kRec * 4);  // records at a time
+        const int vecs = rows * (kRec / 4);                               // 16-byte pieces of one
+        constexpr int kItems = (R * (D / 4) + kPgThreads - 1) / kPgThreads;
+        float4 v[kItems];
+        float M[kItems], L[kItems];
+#pragma unroll
+        for (int x = 0; x < kItems; ++x) {
+          v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          M[x] = neg_inf();
+          L[x] = 0.f;
         }
-        __syncthreads();
-        // items of 4 dims; when they are few, several threads share an item's records
-        const int items = rows * (D / 4);
-        const int share = items >= kPgThreads ? 1 : kPgThreads / items;
-        for (int i0 = 0; i0 < items; i0 += kPgThreads) {
-          const int i = i0 + (share > 1 ? tid % items : tid), part = share > 1 ? tid / items : 0;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int r = i / (D / 4), d = 4 * (i % (D / 4));
-          if (i < items && part < share) {
-#pragma unroll 8
-            for (int k = part; k < nr; k += share) {
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(rec_of(k, r) + kPartHeader + d));
-              const float c = cw[r * nr + k];
-              v = make_float4(fmaf(c, x.x, v.x), fmaf(c, x.y, v.y), fmaf(c, x.z, v.z), fmaf(c, x.w, v.w));
-            }
+        for (int k0 = 0; k0 < nr; k0 += kFit) {
+          const int nk = min(kFit, nr - k0);
+          for (int i = tid; i < nk * vecs; i += kPgThreads) {
+            const int k = i / vecs, j = i - k * vecs;
+            const float *src = a.part + (static_cast<size_t>(c0 + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * R * kRec;
+            cp_async16(smem_u32(smem) + (k * R * kRec + 4 * j) * 4, src + 4 * j, 16);
           }
-          if (share > 1) {
-            sums[tid] = v;
-            __syncthreads();
-            if (tid < items) {
-              for (int k = 1; k < share; ++k) {
-                const float4 x = sums[tid + k * items];
-                v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+          cp_async_commit();
+          cp_async_wait<0>();
+          __syncthreads();
+#pragma unroll
+          for (int x = 0; x < kItems; ++x) {
+            const int i = tid + x * kPgThreads;
+            if (i < rows * (D / 4)) {
+              const float *src = reinterpret_cast<const float *>(smem) + (i / (D / 4)) * kRec;
+              const int d = 4 * (i % (D / 4));
+              float mn = M[x];
+              for (int k = 0; k < nk; ++k) mn = fmaxf(mn, src[k * R * kRec]);
+              const float mm = mn == neg_inf() ? 0.f : mn, c0x = exp2_approx(M[x] - mm);
+              L[x] *= c0x;
+              v[x] = make_float4(v[x].x * c0x, v[x].y * c0x, v[x].z * c0x, v[x].w * c0x);
+              M[x] = mn;
+#pragma unroll 4
+              for (int k = 0; k < nk; ++k) {
+                const float *q = src + k * R * kRec;
+                const float c = exp2_approx(q[0] - mm);
+                const float4 y = *reinterpret_cast<const float4 *>(q + kPartHeader + d);
+                L[x] = fmaf(c, q[1], L[x]);
+                v[x] = make_float4(fmaf(c, y.x, v[x].x), fmaf(c, y.y, v[x].y), fmaf(c, y.z, v[x].z),
+                                   fmaf(c, y.w, v[x].w));
               }
             }
           }
-          if (i < items && part == 0) put(r, d, v, rowM[r], rowL[r]);
+          __syncthreads();
+        }
+#pragma unroll
+        for (int x = 0; x < kItems; ++x) {
+          const int i = tid + x * kPgThreads;
+          if (i < rows * (D / 4)) put(i / (D / 4), 4 * (i % (D / 4)), v[x], M[x], L[x]);
         }
       }
     }
