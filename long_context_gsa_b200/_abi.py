@@ -469,122 +469,149 @@ def gsa_noalloc_status(stream=None) -> int:
 
 
 # ------------------------------------------------- paged raw-token cache
+# A serving loop calls these every few microseconds of GPU time, so the checks
+# of a call that passes them cost one comparison each.
 _CACHE_DT = {GSA_F32: torch.float32, GSA_BF16: torch.bfloat16, GSA_I8: torch.int8, GSA_E4M3: torch.float8_e4m3fn}
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _here(*tensors):
-    """CUDA tensors lie on the current device (their pointers are used on its stream)."""
-    dev = None
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            if dev is None:
-                dev = torch.cuda.current_device()
-            if t.device.index != dev:
-                raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+def _device() -> int:
+    """The current CUDA device (-2 without one: no tensor is on it)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        return -2
 
 
-def _rows(t, dtype, name, n_tok, heads, d, stride):
+def _arg(t, dtype, name, numel, dev, optional=False):
+    """Data pointer of `t` after _ptr's checks, and that it lies on device `dev` (whose stream will use it)."""
+    if (t is not None and t.get_device() == dev and t.dtype is dtype and t.numel() >= numel and t.is_contiguous()):
+        return t.data_ptr()
+    p = _ptr(t, dtype, name, optional, numel)
+    if p is not None:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return None
+
+
+def _rows(t, dtype, name, n_tok, heads, d, stride, dev):
     """Data pointer of token rows [n_tok, heads, d], `stride` elements apart (0: packed)."""
     want = (stride or heads * d, d, 1)
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dim() != 3 or t.shape[0] < n_tok or tuple(t.shape[1:]) != (heads, d):
+    if t.dim() != 3 or t.shape[0] < n_tok or t.shape[1] != heads or t.shape[2] != d:
         raise ValueError(f"{name} must be [>= {n_tok}, {heads}, {d}], got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the GSA path has no CPU implementation)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if n_tok and (t.stride()[2] != 1 or (heads > 1 and t.stride()[1] != d) or (n_tok > 1 and t.stride()[0] != want[0])):
-        raise ValueError(f"{name} has strides {t.stride()}, the descriptor says {want}")
-    return C.c_void_p(t.data_ptr())
+    have = t.stride()
+    if have != want and n_tok and (have[2] != 1 or (heads > 1 and have[1] != d) or (n_tok > 1 and have[0] != want[0])):
+        raise ValueError(f"{name} has strides {have}, the descriptor says {want}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
-def _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table):
+def _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev):
     """The pool's pointer arguments, in the order of the C calls."""
-    dt = _CACHE_DT.get(pdesc.cache_dtype)
-    coded = pdesc.cache_dtype in (GSA_I8, GSA_E4M3)
-    pool = pdesc.n_pages * pdesc.page * desc.hkv
-    ns = pool // desc.chunk if desc.chunk > 0 else 0
-    nt = desc.batch * pdesc.max_pages
-    _here(k_pages, v_pages, k_scale, v_scale, page_table)
-    return (_ptr(k_pages, dt, "k_pages", numel=pool * desc.d), _ptr(v_pages, dt, "v_pages", numel=pool * desc.d),
-            _ptr(k_scale, torch.float32, "k_scale", not coded, ns),
-            _ptr(v_scale, torch.float32, "v_scale", not coded, ns), _ptr(page_table, torch.int32, "page_table", numel=nt))
+    code, page, n_pages = pdesc.cache_dtype, pdesc.page, pdesc.n_pages
+    dt = _CACHE_DT.get(code)
+    coded = code >= GSA_I8
+    rows, chunk = n_pages * page * desc.hkv, desc.chunk
+    ns, n = rows // chunk if chunk > 0 else 0, rows * desc.d
+    return (_arg(k_pages, dt, "k_pages", n, dev), _arg(v_pages, dt, "v_pages", n, dev),
+            _arg(k_scale, _F32, "k_scale", ns, dev, not coded), _arg(v_scale, _F32, "v_scale", ns, dev, not coded),
+            _arg(page_table, _I32, "page_table", desc.batch * pdesc.max_pages, dev))
+
+
+def _tail(ws, stream, dev):
+    """Workspace pointer and bytes, stream."""
+    p, n = _ws(ws)
+    if ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, the current device is cuda:{dev}")
+    return p, n, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
 
 
 def gsa_paged_append(desc, pdesc, adesc, q_new, k_new, v_new, cu_tok, pos, inv_freq, page_table, n_gists, own_len,
                      k_pages, v_pages, k_scale, v_scale, q_out, ws, stream=None):
-    dt, n, i32 = _TORCH_DT[desc.dtype], adesc.n_tok, torch.int32
-    _here(q_new, k_new, v_new, cu_tok, pos, inv_freq, n_gists, own_len, q_out, ws)
-    kp, vp_, ks, vs, table = _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table)
+    dev = _device()
+    dt, n, rot = _TORCH_DT[desc.dtype], adesc.n_tok, adesc.rot_dim
+    B, hq, hkv, d = desc.batch, desc.hq, desc.hkv, desc.d
+    kp, vp, ks, vs, table = _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev)
     q = q_o = None
     if q_new is not None:
-        q = _rows(q_new, dt, "q_new", n, desc.hq, desc.d, adesc.q_stride)
-        q_o = _ptr(q_out, dt, "q_out", numel=n * desc.hq * desc.d)
-    _check("gsa_paged_append", load().gsa_paged_append(
-        C.byref(desc), C.byref(pdesc), C.byref(adesc), q,
-        _rows(k_new, dt, "k_new", n, desc.hkv, desc.d, adesc.k_stride),
-        _rows(v_new, dt, "v_new", n, desc.hkv, desc.d, adesc.v_stride),
-        _ptr(cu_tok, i32, "cu_tok", True, desc.batch + 1), _ptr(pos, i32, "pos", True, n),
-        _ptr(inv_freq, torch.float32, "inv_freq", adesc.rot_dim == 0, adesc.rot_dim // 2),
-        table, _ptr(n_gists, i32, "n_gists", True, desc.batch), _ptr(own_len, i32, "own_len", numel=desc.batch),
-        kp, vp_, ks, vs, q_o, *_ws(ws), _stream(stream)))
+        q = _rows(q_new, dt, "q_new", n, hq, d, adesc.q_stride, dev)
+        q_o = _arg(q_out, dt, "q_out", n * hq * d, dev)
+    st = load().gsa_paged_append(
+        C.byref(desc), C.byref(pdesc), C.byref(adesc), q, _rows(k_new, dt, "k_new", n, hkv, d, adesc.k_stride, dev),
+        _rows(v_new, dt, "v_new", n, hkv, d, adesc.v_stride, dev), _arg(cu_tok, _I32, "cu_tok", B + 1, dev, True),
+        _arg(pos, _I32, "pos", n, dev, True), _arg(inv_freq, _F32, "inv_freq", rot // 2, dev, rot == 0), table,
+        _arg(n_gists, _I32, "n_gists", B, dev, True), _arg(own_len, _I32, "own_len", B, dev), kp, vp, ks, vs, q_o,
+        *_tail(ws, stream, dev))
+    if st:
+        _check("gsa_paged_append", st)
 
 
 def gsa_paged_attend(desc, pdesc, n_q, q, k_pages, v_pages, k_scale, v_scale, page_table, n_gists, own_len, out, lse,
                      ws, stream=None):
-    _here(q, n_gists, own_len, out, lse, ws)
-    nq = max(int(n_q), 0)
-    _check("gsa_paged_attend", load().gsa_paged_attend(
-        C.byref(desc), C.byref(pdesc), int(n_q), _ptr(q, _TORCH_DT[desc.dtype], "q", numel=nq * _n(desc, "q")),
-        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
-        _ptr(n_gists, torch.int32, "n_gists", True, desc.batch),
-        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
-        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=nq * _n(desc, "q")),
-        _ptr(lse, torch.float32, "lse", True, nq * _n(desc, "heads")), *_ws(ws), _stream(stream)))
+    dev = _device()
+    B, rows = desc.batch, desc.batch * desc.hq * max(n_q, 0)
+    n = rows * desc.d
+    st = load().gsa_paged_attend(
+        C.byref(desc), C.byref(pdesc), n_q, _arg(q, _TORCH_DT[desc.dtype], "q", n, dev),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev),
+        _arg(n_gists, _I32, "n_gists", B, dev, True), _arg(own_len, _I32, "own_len", B, dev),
+        _arg(out, _TORCH_DT[desc.out_dtype], "out", n, dev), _arg(lse, _F32, "lse", rows, dev, True),
+        *_tail(ws, stream, dev))
+    if st:
+        _check("gsa_paged_attend", st)
 
 
 def gsa_paged_unfold(desc, pdesc, q, k_pages, v_pages, k_scale, v_scale, page_table, gist_v, n_gists, own_len, sel_idx,
                      sel_score, prior, out, lse, ws, stream=None):
-    dt = _TORCH_DT[desc.dtype]
-    _here(q, gist_v, n_gists, own_len, sel_idx, sel_score, out, lse, ws)
-    _check("gsa_paged_unfold", load().gsa_paged_unfold(
-        C.byref(desc), C.byref(pdesc), _ptr(q, dt, "q", numel=_n(desc, "q")),
-        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
-        _ptr(gist_v, dt, "gist_v", True, _n(desc, "gists")), _ptr(n_gists, torch.int32, "n_gists", numel=desc.batch),
-        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
-        _ptr(sel_idx, torch.int32, "sel_idx", True, _n(desc, "sel")),
-        _ptr(sel_score, torch.float32, "sel_score", True, _n(desc, "sel")), int(prior),
-        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=_n(desc, "q")),
-        _ptr(lse, torch.float32, "lse", True, _n(desc, "heads")), *_ws(ws), _stream(stream)))
+    dev, dt = _device(), _TORCH_DT[desc.dtype]
+    B, rows, d = desc.batch, desc.batch * desc.hq, desc.d
+    n, sel = rows * d, rows * desc.topk
+    st = load().gsa_paged_unfold(
+        C.byref(desc), C.byref(pdesc), _arg(q, dt, "q", n, dev),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev),
+        _arg(gist_v, dt, "gist_v", B * desc.hkv * desc.n_max * d, dev, True), _arg(n_gists, _I32, "n_gists", B, dev),
+        _arg(own_len, _I32, "own_len", B, dev), _arg(sel_idx, _I32, "sel_idx", sel, dev, True),
+        _arg(sel_score, _F32, "sel_score", sel, dev, True), prior, _arg(out, _TORCH_DT[desc.out_dtype], "out", n, dev),
+        _arg(lse, _F32, "lse", rows, dev, True), *_tail(ws, stream, dev))
+    if st:
+        _check("gsa_paged_unfold", st)
 
 
 def gsa_paged_decode(desc, pdesc, q, gist_k, gist_v, k_pages, v_pages, k_scale, v_scale, page_table, n_gists, own_len,
                      out, lse=None, sel_idx=None, sel_score=None, ws=None, stream=None):
-    dt = _TORCH_DT[desc.dtype]
-    _here(q, gist_k, gist_v, n_gists, own_len, out, lse, sel_idx, sel_score, ws)
-    _check("gsa_paged_decode", load().gsa_paged_decode(
-        C.byref(desc), C.byref(pdesc), _ptr(q, dt, "q", numel=_n(desc, "q")),
-        _ptr(gist_k, dt, "gist_k", numel=_n(desc, "gists")), _ptr(gist_v, dt, "gist_v", numel=_n(desc, "gists")),
-        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
-        _ptr(n_gists, torch.int32, "n_gists", numel=desc.batch),
-        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
-        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=_n(desc, "q")),
-        _ptr(lse, torch.float32, "lse", True, _n(desc, "heads")),
-        _ptr(sel_idx, torch.int32, "sel_idx", True, _n(desc, "sel")),
-        _ptr(sel_score, torch.float32, "sel_score", True, _n(desc, "sel")), *_ws(ws), _stream(stream)))
+    dev, dt = _device(), _TORCH_DT[desc.dtype]
+    B, rows, d = desc.batch, desc.batch * desc.hq, desc.d
+    n, sel, gists = rows * d, rows * desc.topk, B * desc.hkv * desc.n_max * d
+    st = load().gsa_paged_decode(
+        C.byref(desc), C.byref(pdesc), _arg(q, dt, "q", n, dev), _arg(gist_k, dt, "gist_k", gists, dev),
+        _arg(gist_v, dt, "gist_v", gists, dev),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev),
+        _arg(n_gists, _I32, "n_gists", B, dev), _arg(own_len, _I32, "own_len", B, dev),
+        _arg(out, _TORCH_DT[desc.out_dtype], "out", n, dev), _arg(lse, _F32, "lse", rows, dev, True),
+        _arg(sel_idx, _I32, "sel_idx", sel, dev, True), _arg(sel_score, _F32, "sel_score", sel, dev, True),
+        *_tail(ws, stream, dev))
+    if st:
+        _check("gsa_paged_decode", st)
 
 
 def gsa_paged_gist_step(desc, pdesc, q, k_new, v_new, gist_k, gist_v, k_pages, v_pages, k_scale, v_scale, page_table,
                         n_gists, own_len, out, lse, ws, stream=None):
-    dt = _TORCH_DT[desc.dtype]
-    _here(q, k_new, v_new, gist_k, gist_v, n_gists, own_len, out, lse, ws)
-    _check("gsa_paged_gist_step", load().gsa_paged_gist_step(
-        C.byref(desc), C.byref(pdesc), _ptr(q, dt, "q", numel=_n(desc, "q")),
-        _ptr(k_new, dt, "k_new", numel=_n(desc, "kv_new")), _ptr(v_new, dt, "v_new", numel=_n(desc, "kv_new")),
-        _ptr(gist_k, dt, "gist_k", numel=_n(desc, "gists")), _ptr(gist_v, dt, "gist_v", numel=_n(desc, "gists")),
-        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table),
-        _ptr(n_gists, torch.int32, "n_gists", numel=desc.batch),
-        _ptr(own_len, torch.int32, "own_len", numel=desc.batch),
-        _ptr(out, _TORCH_DT[desc.out_dtype], "out", numel=_n(desc, "q")),
-        _ptr(lse, torch.float32, "lse", True, _n(desc, "heads")), *_ws(ws), _stream(stream)))
+    dev, dt = _device(), _TORCH_DT[desc.dtype]
+    B, rows, d, hkv = desc.batch, desc.batch * desc.hq, desc.d, desc.hkv
+    n, new, gists = rows * d, B * hkv * d, B * hkv * desc.n_max * d
+    st = load().gsa_paged_gist_step(
+        C.byref(desc), C.byref(pdesc), _arg(q, dt, "q", n, dev), _arg(k_new, dt, "k_new", new, dev),
+        _arg(v_new, dt, "v_new", new, dev), _arg(gist_k, dt, "gist_k", gists, dev),
+        _arg(gist_v, dt, "gist_v", gists, dev),
+        *_cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev),
+        _arg(n_gists, _I32, "n_gists", B, dev), _arg(own_len, _I32, "own_len", B, dev),
+        _arg(out, _TORCH_DT[desc.out_dtype], "out", n, dev), _arg(lse, _F32, "lse", rows, dev, True),
+        *_tail(ws, stream, dev))
+    if st:
+        _check("gsa_paged_gist_step", st)

@@ -33,8 +33,7 @@ constexpr int kUnfoldSplitMax = 32;  // partial slots per row from the unfold pa
 constexpr int kHgsaSplitMax = 32;    // partial slots per row from the H-GSA pass
 constexpr int kTopkSmemCap = 16384;  // keys kept in shared memory by the top-k kernel
 constexpr int kMaxTopk = kTopkMax;
-constexpr int kPgMaxQueries = 64;                     // query tokens per sequence of the paged attention
-constexpr int kPgMaxGroups = kPgMaxQueries * 16 / 8;  // its segments of 8 query rows per kv head
+constexpr int kPgMaxQueries = 64;    // query tokens per sequence of the paged attention
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -50,7 +49,7 @@ struct Layout {
   size_t meta2_scores = 0, meta2_idx = 0, cand1_scores = 0, cand1_ids = 0, cand1_count = 0;
   size_t pf_stats = 0, pf_gist = 0, pf_vh = 0, pf_ovf = 0;
   size_t gs_cur = 0, gs_plus = 0;
-  size_t pg_append = 0, pg_seg = 0, pg_part = 0;
+  size_t pg_append = 0, pg_joins = 0, pg_part = 0;
   size_t total = 0;
 };
 
@@ -154,7 +153,7 @@ Layout layout(const gsa_desc *d, int32_t op, const gsa_hdesc *h) {
   }
   if (op == GSA_OP_PAGED) {
     take(L.pg_append, 256);
-    take(L.pg_seg, static_cast<size_t>(d->batch) * d->hkv * kPgMaxGroups * 4);
+    take(L.pg_joins, static_cast<size_t>(kPgMaxCtas) * sizeof(int4));
     take(L.pg_part, static_cast<size_t>(kPgMaxCtas) * 2 * kPgMaxRows * rec);
     take(L.gs_cur, static_cast<size_t>(d->batch) * 4);  // gsa_paged_gist_step runs in this workspace too
     take(L.gs_plus, static_cast<size_t>(d->batch) * 4);

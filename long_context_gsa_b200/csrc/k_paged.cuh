@@ -36,8 +36,6 @@
 // scales one tile behind them.
 #pragma once
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "k_unfold.cuh"  // UnfoldArgs, ready list
 
@@ -617,14 +615,20 @@ struct PgWarp {
 // The rows of all (sequence, kv head, group of 8 NT query rows) segments, in
 // steps of 32 rows a warp, form one line that the CTAs cut into equal parts
 // (the lengths are on the device, so the cut is too): ragged batches and
-// single long sequences load every SM alike.  A segment inside one CTA is
-// written directly; one that several CTAs share is joined by the last of them
-// to arrive (an atomic counter, no waiting) from partial records, in CTA
-// order, so the result does not depend on who was last.  CTAs of 4 warps, 3
-// or 4 on an SM: one joins its warps while the others stream.
+// single long sequences load every SM alike.  A segment begins with kPgHead
+// empty steps on that line, about what starting one costs a CTA, and one of up
+// to kPgWhole steps is not cut.  A segment inside one CTA is written
+// directly; of one that several CTAs share each leaves a partial record, which
+// k_paged_join adds up in CTA order.  (Joining by the last CTA to arrive took
+// 10 us of 108 at 4 x 128K rows, 4 query heads: one CTA, 28 records, one
+// dependent load behind the other; the second kernel has a warp a row and
+// takes 3.)  CTAs of 4 warps, 3 or 4 on an SM: one joins its warps while the
+// others stream.
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgStep = 32 * kPgWarps;  // rows of one CTA step
+constexpr uint32_t kPgHead = 2;         // empty steps before a segment's rows
+constexpr uint32_t kPgWhole = 4;        // steps of a segment that is not cut
 constexpr int kPgMaxCtas = 640;         // bound of the grid (partial slots in the workspace)
 constexpr int kPgMaxBatch = 8192;       // prefix sums in shared memory
 constexpr int kPgMaxRows = 16;          // query rows of a segment
@@ -637,7 +641,7 @@ struct PagedAttendArgs {
   int32_t B, n_q, hq, group, rg, chunk, n_max, t_max, min_steps;
   float scale_log2;
   float *part;                 // [ctas][2][8 NT][D + 4]
-  uint32_t *counters;          // [B * hkv * rg]
+  int4 *joins;                 // [ctas]: (b, segment, last CTA, 0) of the cut segment that begins in a CTA; b < 0: none
   uint32_t *status;
   void *out;                   // [B, n_q, hq, D]
   int32_t out_bf16;
@@ -650,6 +654,26 @@ __device__ __forceinline__ int paged_len(const int32_t *n_gists, const int32_t *
   int64_t n = max(__ldcg(own_len + b), 0);
   if (n_gists) n += static_cast<int64_t>(min(max(__ldcg(n_gists + b), 0), n_max)) * chunk;
   return static_cast<int>(n < t_max ? n : t_max);
+}
+
+// Query row x (token x / group, head x % group of the kv head) of sequence b: its row in q and out.
+__device__ __forceinline__ size_t paged_row(const PagedAttendArgs &a, int b, int kvh, int x) {
+  return (static_cast<size_t>(b) * a.n_q + x / a.group) * a.hq + kvh * a.group + x % a.group;
+}
+
+// Four dims of a finished row: sum of weighted values v, base-2 maximum M and sum L of the weights.
+template <int D>
+__device__ __forceinline__ void paged_put(const PagedAttendArgs &a, size_t row, int d, float4 v, float M, float L) {
+  const size_t o = row * D + d;
+  const float i = L != 0.f ? 1.f / L : 0.f;
+  if (a.out_bf16) {
+    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + o);
+    dst[0] = __floats2bfloat162_rn(v.x * i, v.y * i);
+    dst[1] = __floats2bfloat162_rn(v.z * i, v.w * i);
+  } else {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(v.x * i, v.y * i, v.z * i, v.w * i);
+  }
+  if (d == 0 && a.lse) a.lse[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : neg_inf();
 }
 
 // Exclusive prefix sums of count(b), b < B, in pre[0 .. B] (shared), by the
@@ -705,20 +729,22 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
   using Query = typename Warp::Query;
   constexpr int R = 8 * NT, kRec = D + kPartHeader;
   static_assert(PgCfg<D>::kRing >= R * kRec * 4, "the warps' results fit over the rings");
+  static_assert(kPgWarps * PgCfg<D>::kRing >= 8 * kPgMaxCtas * 4, "the weights of a join fit over the rings");
   extern __shared__ __align__(128) uint8_t smem[];
   Query &qs = *reinterpret_cast<Query *>(smem + kPgWarps * PgCfg<D>::kRing);
   uint32_t *pre = reinterpret_cast<uint32_t *>(smem + paged_attend_smem<D, FMT, QF32, NT>());
   int *lens = reinterpret_cast<int *>(pre + a.B + 1);
   float(*red)[R][kRec] = reinterpret_cast<float(*)[R][kRec]>(smem);
   __shared__ float wgt[R][kPgWarps], rowM[R], rowL[R];
-  __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int per_b = a.kv.hkv * a.rg;
   pdl_wait();
+  pdl_trigger();  // the join kernel waits for this grid; its CTAs fit once ours leave
   paged_prefix<kPgThreads>(pre, a.B, [&](int b) {
     const int len = paged_len(a.n_gists, a.own_len, b, a.n_max, a.chunk, a.t_max);
     lens[b] = len;
-    return static_cast<uint32_t>(per_b) * static_cast<uint32_t>((len + kPgStep - 1) / kPgStep);
+    const uint32_t steps = static_cast<uint32_t>((len + kPgStep - 1) / kPgStep);
+    return static_cast<uint32_t>(per_b) * (steps ? steps + kPgHead : 0u);
   });
   const uint32_t total = pre[a.B];
   const uint32_t ctas = min(gridDim.x, max(1u, (total + a.min_steps - 1) / a.min_steps));
@@ -731,26 +757,38 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
       if (a.lse)
         for (int i = tid; i < a.n_q * a.hq; i += kPgThreads) a.lse[row0 + i] = neg_inf();
     }
-  if (cta >= ctas) return;
-  const uint32_t p0 = static_cast<uint32_t>(static_cast<uint64_t>(total) * cta / ctas);
-  const uint32_t p1 = static_cast<uint32_t>(static_cast<uint64_t>(total) * (cta + 1) / ctas);
+  int4 join = make_int4(-1, 0, 0, 0);
+  if (cta >= ctas) {
+    if (tid == 0) a.joins[cta] = join;
+    return;
+  }
+  // where CTA c's part begins: a cut inside a short segment moves to its start
+  auto cut = [&](uint32_t c) {
+    const uint32_t p = static_cast<uint32_t>(static_cast<uint64_t>(total) * c / ctas);
+    if (p == total) return p;
+    const int b = paged_find(pre, a.B, p);
+    const uint32_t steps = (pre[b + 1] - pre[b]) / per_b;
+    return steps > kPgWhole + kPgHead ? p : p - (p - pre[b]) % steps;
+  };
+  const uint32_t p0 = cut(cta), p1 = cut(cta + 1);
   Warp w;
   w.ring = smem_u32(smem) + warp * PgCfg<D>::kRing;
   for (uint32_t p = p0; p < p1;) {
     const int b = paged_find(pre, a.B, p);
-    const uint32_t steps = (pre[b + 1] - pre[b]) / per_b;
+    const uint32_t steps = (pre[b + 1] - pre[b]) / per_b;  // with the head
     const uint32_t seg = (p - pre[b]) / steps;
-    const uint32_t seg0 = pre[b] + seg * steps, seg1 = seg0 + steps;
-    const uint32_t s0 = p - seg0, s1 = min(p1, seg1) - seg0;
-    p = seg0 + s1;
+    const uint32_t seg0 = pre[b] + seg * steps + kPgHead, seg1 = seg0 + steps - kPgHead;  // its rows
+    const uint32_t begin = max(p, seg0);
+    p = min(p1, seg1);
+    if (p <= begin) {  // this part ends inside the head
+      p = p1;
+      continue;
+    }
+    const uint32_t s0 = begin - seg0, s1 = p - seg0;
     const int kvh = seg / a.rg, rg = seg % a.rg;
     const int len = lens[b];
     const int rows = min(R, a.n_q * a.group - rg * R);
-    // query row r of the segment -> its row in q and out
-    auto out_row = [&](int r) {
-      const int x = rg * R + r;
-      return (static_cast<size_t>(b) * a.n_q + x / a.group) * a.hq + kvh * a.group + x % a.group;
-    };
+    auto out_row = [&](int r) { return paged_row(a, b, kvh, rg * R + r); };
     int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -810,23 +848,12 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
       rowL[tid] = L;
     }
     __syncthreads();
-    const uint32_t c0 = static_cast<uint32_t>(((static_cast<uint64_t>(seg0) + 1) * ctas - 1) / total);
-    const uint32_t c1 = static_cast<uint32_t>((static_cast<uint64_t>(seg1) * ctas - 1) / total);
-    const bool whole = c0 == c1;
-    auto put = [&](int r, int d, float4 v, float M, float L) {  // 4 dims of a finished row
-      const size_t o = out_row(r) * D + d;
-      const float i = L != 0.f ? 1.f / L : 0.f;
-      if (a.out_bf16) {
-        __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + o);
-        dst[0] = __floats2bfloat162_rn(v.x * i, v.y * i);
-        dst[1] = __floats2bfloat162_rn(v.z * i, v.w * i);
-      } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(v.x * i, v.y * i, v.z * i, v.w * i);
-      }
-      if (d == 0 && a.lse) a.lse[out_row(r)] = L != 0.f ? (M + __log2f(L)) * kLn2 : neg_inf();
-    };
+    const bool whole = begin == seg0 && p == seg1;
     // this CTA's record: slot 1 if the segment starts in its part, else slot 0
-    float *rec = a.part + (static_cast<size_t>(cta) * 2 + (cta == c0 ? 1 : 0)) * R * kRec;
+    float *rec = a.part + (static_cast<size_t>(cta) * 2 + (begin == seg0 ? 1 : 0)) * R * kRec;
+    if (!whole && begin == seg0)
+      join = make_int4(b, static_cast<int>(seg),
+                       static_cast<int>((static_cast<uint64_t>(seg1) * ctas - 1) / total), 0);
     for (int i = tid; i < rows * (D / 4); i += kPgThreads) {
       const int r = i / (D / 4), d = 4 * (i % (D / 4));
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -837,86 +864,79 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
         v = make_float4(fmaf(c, x.x, v.x), fmaf(c, x.y, v.y), fmaf(c, x.z, v.z), fmaf(c, x.w, v.w));
       }
       if (whole) {
-        put(r, d, v, rowM[r], rowL[r]);
+        paged_put<D>(a, out_row(r), d, v, rowM[r], rowL[r]);
       } else {
         float *dst = rec + static_cast<size_t>(r) * kRec;
         *reinterpret_cast<float4 *>(dst + kPartHeader + d) = v;
         if (d == 0) *reinterpret_cast<float2 *>(dst) = make_float2(rowM[r], rowL[r]);
       }
     }
-    if (!whole) {
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        uint32_t *counter = a.counters + (static_cast<size_t>(b) * per_b + seg);
-        const bool last = atomicAdd(counter, 1u) == c1 - c0;
-        if (last) {
-          __threadfence();
-          *counter = 0u;
-        }
-        last_s = last;
-      }
-      __syncthreads();
-      if (last_s) {
-        // join the records of CTAs c0 .. c1 (c0's in slot 1), in that order: all of them (or as many as the rings
-        // hold) are copied to shared memory at once, then summed
-        const int nr = static_cast<int>(c1 - c0) + 1;
-        constexpr int kFit = kPgWarps * PgCfg<D>::kRing / (R * kRec * 4);  // records at a time
-        const int vecs = rows * (kRec / 4);                               // 16-byte pieces of one
-        constexpr int kItems = (R * (D / 4) + kPgThreads - 1) / kPgThreads;
-        float4 v[kItems];
-        float M[kItems], L[kItems];
-#pragma unroll
-        for (int x = 0; x < kItems; ++x) {
-          v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-          M[x] = neg_inf();
-          L[x] = 0.f;
-        }
-        for (int k0 = 0; k0 < nr; k0 += kFit) {
-          const int nk = min(kFit, nr - k0);
-          for (int i = tid; i < nk * vecs; i += kPgThreads) {
-            const int k = i / vecs, j = i - k * vecs;
-            const float *src = a.part + (static_cast<size_t>(c0 + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * R * kRec;
-            cp_async16(smem_u32(smem) + (k * R * kRec + 4 * j) * 4, src + 4 * j, 16);
-          }
-          cp_async_commit();
-          cp_async_wait<0>();
-          __syncthreads();
-#pragma unroll
-          for (int x = 0; x < kItems; ++x) {
-            const int i = tid + x * kPgThreads;
-            if (i < rows * (D / 4)) {
-              const float *src = reinterpret_cast<const float *>(smem) + (i / (D / 4)) * kRec;
-              const int d = 4 * (i % (D / 4));
-              float mn = M[x];
-              for (int k = 0; k < nk; ++k) mn = fmaxf(mn, src[k * R * kRec]);
-              const float mm = mn == neg_inf() ? 0.f : mn, c0x = exp2_approx(M[x] - mm);
-              L[x] *= c0x;
-              v[x] = make_float4(v[x].x * c0x, v[x].y * c0x, v[x].z * c0x, v[x].w * c0x);
-              M[x] = mn;
-#pragma unroll 4
-              for (int k = 0; k < nk; ++k) {
-                const float *q = src + k * R * kRec;
-                const float c = exp2_approx(q[0] - mm);
-                const float4 y = *reinterpret_cast<const float4 *>(q + kPartHeader + d);
-                L[x] = fmaf(c, q[1], L[x]);
-                v[x] = make_float4(fmaf(c, y.x, v[x].x), fmaf(c, y.y, v[x].y), fmaf(c, y.z, v[x].z),
-                                   fmaf(c, y.w, v[x].w));
-              }
-            }
-          }
-          __syncthreads();
-        }
-#pragma unroll
-        for (int x = 0; x < kItems; ++x) {
-          const int i = tid + x * kPgThreads;
-          if (i < rows * (D / 4)) put(i / (D / 4), 4 * (i % (D / 4)), v[x], M[x], L[x]);
-        }
-      }
-    }
     __syncthreads();  // results, queries and row sums are read: the next segment may overwrite them
   }
-  pdl_trigger();
+  if (tid == 0) a.joins[cta] = join;
+}
+
+// Grid (ctas, NT) behind k_paged_attend: CTA (c, nt) adds up 8 rows of the cut
+// segment that begins in c's part, a warp a row.  The records lie equally
+// spaced (c's own in slot 1, the others in slot 0); the first kBatch of them
+// are fetched while the weights (a record a lane) are made.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) k_paged_join(const PagedAttendArgs a) {
+  constexpr int R = 8 * NT, kRec = D + kPartHeader, kStride = 2 * R * kRec;
+  constexpr int kSub = 128 / D, kBatch = 16;  // records side by side in a warp, and in flight a lane
+  extern __shared__ float cw[];               // [8][ctas] weights
+  pdl_wait();
+  const int4 join = __ldcg(a.joins + blockIdx.x);
+  if (join.x < 0) return;
+  const int kvh = join.y / a.rg, rg = join.y % a.rg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = rg * R + 8 * blockIdx.y + warp;
+  if (x >= a.n_q * a.group) return;
+  const int nr = join.z - static_cast<int>(blockIdx.x) + 1, sub = lane / (D / 4), d = 4 * (lane % (D / 4));
+  const float *rec0 = a.part + static_cast<size_t>(blockIdx.x) * kStride + (8 * blockIdx.y + warp) * kRec;
+  auto rec_of = [&](int k) { return rec0 + (k == 0 ? R * kRec : static_cast<size_t>(k) * kStride); };
+  float4 y[kBatch];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j * kSub + sub;
+      if (k < nr) y[j] = __ldcg(reinterpret_cast<const float4 *>(rec_of(k) + kPartHeader + d));
+    }
+  };
+  fetch(0);
+  float *w = cw + warp * gridDim.x;
+  float M = neg_inf(), L = 0.f;
+  for (int k = lane; k < nr; k += 32) {
+    const float2 h = __ldcg(reinterpret_cast<const float2 *>(rec_of(k)));
+    // one pass: the sum is kept relative to the largest so far
+    const float mn = fmaxf(M, h.x), mm = mn == neg_inf() ? 0.f : mn;
+    L = fmaf(L, exp2_approx(M - mm), exp2_approx(h.x - mm) * h.y);
+    M = mn;
+    w[k] = h.x;
+  }
+  const float mt = warp_max(M), mm = mt == neg_inf() ? 0.f : mt;
+  L = warp_sum(L * exp2_approx(M - mm));
+  for (int k = lane; k < nr; k += 32) w[k] = exp2_approx(w[k] - mm);
+  __syncwarp();
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < nr; k0 += kBatch * kSub) {
+    if (k0 > 0) fetch(k0);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j * kSub + sub;
+      if (k < nr) {
+        const float c = w[k];
+        v = make_float4(fmaf(c, y[j].x, v.x), fmaf(c, y[j].y, v.y), fmaf(c, y[j].z, v.z), fmaf(c, y[j].w, v.w));
+      }
+    }
+  }
+#pragma unroll
+  for (int o = D / 4; o < 32; o <<= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+  }
+  if (sub == 0) paged_put<D>(a, paged_row(a, join.x, kvh, x), d, v, mt, L);
 }
 
 // ------------------------------------------------------------------ unfolding

@@ -3,6 +3,8 @@
 // gsa_api.cu behind its own entry points, whose helpers it uses.
 #pragma once
 
+#include <atomic>
+
 namespace gsa {
 namespace {
 
@@ -64,12 +66,36 @@ gsa_status paged_variant(const gsa_desc *d, const gsa_pdesc *p, Fn fn) {
   return p->cache_dtype == GSA_I8 ? with(D128(), I8()) : with(D128(), E4());
 }
 
+// resident_ctas of one kernel, remembered for each device and amount of shared
+// memory asked for last (the queries cost microseconds, as much as a small
+// call's kernel).
+struct SlotCache {
+  static constexpr int kDevices = 16;
+  std::atomic<uint64_t> known[kDevices] = {};  // smem << 32 | CTAs
+  template <typename Kern>
+  int get(Kern kern, int threads, size_t smem) {
+    int dev = -1;
+    const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices;
+    if (keep) {
+      const uint64_t v = known[dev].load(std::memory_order_relaxed);
+      if (v && (v >> 32) == smem) return static_cast<int>(v & 0xffffffffu);
+    }
+    const int n = resident_ctas(kern, threads, smem);
+    if (keep) known[dev].store(static_cast<uint64_t>(smem) << 32 | static_cast<uint32_t>(n), std::memory_order_relaxed);
+    return n;
+  }
+};
+
 template <int D, int FMT, bool QF32, bool HILO, int NT>
 gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
   const size_t smem = paged_attend_smem<D, FMT, QF32, NT>() + (2 * static_cast<size_t>(pa.B) + 1) * 4;
   const auto kern = k_paged_attend<D, FMT, QF32, HILO, NT>;
-  const int grid = std::min(kPgMaxCtas, resident_ctas(kern, kPgThreads, smem));
-  return launch(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa);
+  static SlotCache cache;
+  const int grid = std::min(kPgMaxCtas, cache.get(kern, kPgThreads, smem));
+  GSA_TRY(launch(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa));
+  // no segment can have been cut when the longest is short
+  if (pa.t_max <= static_cast<int>(kPgWhole) * kPgStep) return GSA_OK;
+  return launch(k_paged_join<D, NT>, dim3(grid, NT), dim3(256), static_cast<size_t>(grid) * 8 * 4, stream, pa);
 }
 
 gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q, const void *k, const void *v,
@@ -113,7 +139,8 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
     // residency with the largest list share (one split), then the share of the chosen split count; a split is
     // not made smaller than one 32-row tile a warp
     const int k1 = std::max(1, ua.k);
-    const int slots = resident_ctas(kern, kUnfoldThreads, paged_unfold_smem<D, F, Q>(k1));
+    static SlotCache cache;
+    const int slots = cache.get(kern, kUnfoldThreads, paged_unfold_smem<D, F, Q>(k1));
     const int most = std::max(1, static_cast<int>(static_cast<int64_t>(k1) * d->chunk / (32 * kPuWarps)));
     ua.n_split = one_wave_splits(d->batch * d->hq, slots, std::min(std::min(kUnfoldSplitMax, k1), most));
     return launch(kern, dim3(ua.n_split, d->hq, d->batch), dim3(kUnfoldThreads),
@@ -128,7 +155,8 @@ gsa_status launch_append(const AppendArgs &aa, void *stream) {
   const int64_t most = std::min<int64_t>(aa.n_tok, aa.n_tok / chunk + 2 * static_cast<int64_t>(aa.B));
   const size_t smem = static_cast<size_t>(chunk) * (aa.rot / 2) * 8 + (static_cast<size_t>(aa.B) + 1) * 4;
   const auto kern = k_paged_append<D, T, FMT>;
-  const int slots = resident_ctas(kern, kApThreads, smem);
+  static SlotCache cache;
+  const int slots = cache.get(kern, kApThreads, smem);
   const int x = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, slots)));
   // few blocks: several CTAs share the heads of each, one task a warp
   const int rows = static_cast<int>((aa.n_tok + most - 1) / most);
@@ -249,7 +277,8 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   // 8 query rows a segment, or 16 when there are more
   const bool wide = rows > 8;
   const int rg = cdiv(rows, wide ? 16 : 8);
-  if (static_cast<int64_t>(desc->batch) * desc->hkv * rg >= (int64_t(1) << 31) / cdiv(desc->t_max, kPgStep))
+  if (static_cast<int64_t>(desc->batch) * desc->hkv * rg >=
+      (int64_t(1) << 31) / (cdiv(desc->t_max, kPgStep) + static_cast<int>(kPgHead)))
     return GSA_ERR_UNSUPPORTED;  // steps are counted in 32 bits
   PagedAttendArgs pa;
   pa.kv = paged_kv(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table);
@@ -267,7 +296,7 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   pa.min_steps = 2;
   pa.scale_log2 = resolve_scale(desc) * kLog2e;
   pa.part = reinterpret_cast<float *>(at(ws, L.pg_part));
-  pa.counters = reinterpret_cast<uint32_t *>(at(ws, L.pg_seg));
+  pa.joins = reinterpret_cast<int4 *>(at(ws, L.pg_joins));
   pa.status = reinterpret_cast<uint32_t *>(at(ws, L.status));
   pa.out = out;
   pa.out_bf16 = desc->out_dtype == GSA_BF16;

@@ -1,7 +1,6 @@
 """What the paged cache's calls refuse, before anything is enqueued (CPU only:
 no kernel is launched; see test_abi.py for the fake addresses)."""
 import ctypes as C
-from types import SimpleNamespace
 
 import pytest
 import torch
@@ -138,7 +137,7 @@ def test_reader_pointers_and_counts(lib):
     assert _calls(lib, huge, _pdesc(page=1 << 20, max_pages=256))["attend"]() == 2
 
 
-def test_binding_checks(lib, monkeypatch):
+def test_binding_checks(lib):
     from long_context_gsa_b200 import _abi
     d, p = _desc(), _pdesc()
     short = torch.zeros(7, dtype=torch.bfloat16)
@@ -147,34 +146,50 @@ def test_binding_checks(lib, monkeypatch):
     with pytest.raises(ValueError, match="q holds 7"):
         _abi.gsa_paged_attend(d, p, 1, short, codes, codes, scale, scale, t, None, t, t, t, t)
     with pytest.raises(ValueError, match="k_pages holds 4"):
-        _abi._cache(d, p, t, codes, scale, scale, t)
+        _abi._cache(d, p, t, codes, scale, scale, t, 0)
     with pytest.raises(ValueError, match="CUDA tensor"):
-        _abi._cache(d, p, codes, codes, scale, scale, t)
+        _abi._cache(d, p, codes, codes, scale, scale, t, 0)
     with pytest.raises(ValueError, match="must be"):
-        _abi._rows(torch.zeros((3, 2, 128)), torch.float32, "k_new", 4, 2, 128, 0)
+        _abi._rows(torch.zeros((3, 2, 128)), torch.float32, "k_new", 4, 2, 128, 0, 0)
     with pytest.raises(ValueError, match="CUDA tensor"):
-        _abi._rows(torch.zeros((4, 2, 128)), torch.float32, "k_new", 4, 2, 128, 0)
+        _abi._rows(torch.zeros((4, 2, 128)), torch.float32, "k_new", 4, 2, 128, 0, 0)
 
-    class Fake(SimpleNamespace):  # a CUDA tensor's attributes
-        def dim(self):
-            return len(self.shape)
+    class Fake(torch.Tensor):  # a CUDA tensor's attributes
+        is_cuda, where, strides = True, 0, None
+
+        def get_device(self):
+            return self.where
 
         def stride(self):
-            return self.strides
+            return self.strides or super().stride()
 
         def data_ptr(self):
             return A
 
-    ok = dict(is_cuda=True, dtype=torch.float32, shape=(4, 2, 128))
-    assert _abi._rows(Fake(strides=(256, 128, 1), **ok), torch.float32, "k", 4, 2, 128, 0).value == A
-    assert _abi._rows(Fake(strides=(1024, 128, 1), **ok), torch.float32, "k", 4, 2, 128, 1024).value == A
+    def fake(shape=(4, 2, 128), strides=None, where=0, dtype=torch.float32):
+        f = torch.zeros(shape, dtype=dtype).as_subclass(Fake)
+        f.strides, f.where = strides, where
+        return f
+
+    def rows(strides=None, stride=0, dev=0, dtype=torch.float32):
+        return _abi._rows(fake(strides=strides, dtype=dtype), torch.float32, "k", 4, 2, 128, stride, dev)
+
+    assert rows() == A and rows((1024, 128, 1), 1024) == A
     for strides in ((1024, 128, 1), (256, 256, 1), (256, 128, 2)):
         with pytest.raises(ValueError, match="strides"):
-            _abi._rows(Fake(strides=strides, **ok), torch.float32, "k", 4, 2, 128, 0)
+            rows(strides)
     with pytest.raises(TypeError):
-        _abi._rows(Fake(strides=(256, 128, 1), **ok), torch.bfloat16, "k", 4, 2, 128, 0)
-    # a tensor on another device than the current one
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    _abi._here(Fake(is_cuda=True, device=SimpleNamespace(index=0)), None, t)
-    with pytest.raises(ValueError, match="current device"):
-        _abi._here(Fake(is_cuda=True, device=SimpleNamespace(index=1)))
+        rows(dtype=torch.bfloat16)
+    # tensors on another device than the current one
+    assert _abi._arg(fake(), torch.float32, "x", 1024, 0) == A
+    for call in (lambda: rows(dev=1), lambda: _abi._arg(fake(), torch.float32, "x", 1024, 1),
+                 lambda: _abi._tail(fake(), None, 1)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    with pytest.raises(ValueError, match="holds 1024"):
+        _abi._arg(fake(), torch.float32, "x", 1025, 0)
+    with pytest.raises(TypeError):
+        _abi._arg(fake(), torch.int32, "x", 1, 0)
+    assert _abi._arg(None, torch.int32, "x", 1, 0, True) is None
+    with pytest.raises(ValueError, match="required"):
+        _abi._arg(None, torch.int32, "x", 1, 0)
