@@ -268,6 +268,7 @@ struct PgWarp {
   uint32_t off;    // its row in that page
   float sck, scv;  // scales of this lane's key in the tile copied last
   uint32_t ring;
+  static constexpr uint32_t kNoRow = 0xffffffffu;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -290,27 +291,30 @@ struct PgWarp {
     }
   }
 
-  // Copy the fetched tile into stage st.  A key whose page is not in the
-  // pool is left out and flagged.
-  __device__ __forceinline__ void copy(const PagedKV &kv, int kvh, int st, bool wanted, uint32_t *status) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // The pool row of the fetched key, kNoRow without one (a page outside the
+  // pool is flagged); its scales are fetched.
+  __device__ __forceinline__ uint32_t locate(const PagedKV &kv, int kvh, bool wanted, uint32_t *status) {
     const bool live = static_cast<uint32_t>(pid) < static_cast<uint32_t>(kv.n_pages);
     if (wanted && !live) flag_error(status, GSA_DEVERR_BAD_INDEX);
-    const uint32_t ph = live ? static_cast<uint32_t>(pid) * kv.hkv + kvh : 0u;
-    const uint32_t prow = live ? ph * kv.page.d + off : 0xffffffffu;
     sck = scv = 0.f;
-    if (live) {
-      const size_t i = static_cast<size_t>(ph) * kv.blocks + kv.chunk.div(off);
-      sck = __ldcg(kv.ks + i);
-      scv = __ldcg(kv.vs + i);
-    }
+    if (!live) return kNoRow;
+    const uint32_t ph = static_cast<uint32_t>(pid) * kv.hkv + kvh;
+    const size_t i = static_cast<size_t>(ph) * kv.blocks + kv.chunk.div(off);
+    sck = __ldcg(kv.ks + i);
+    scv = __ldcg(kv.vs + i);
+    return ph * kv.page.d + off;
+  }
+
+  // Copy the tile whose keys lie at pool rows prow (one a lane) into stage st.
+  __device__ __forceinline__ void copy(const PagedKV &kv, int st, uint32_t prow) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t base = ring + st * Cfg::kStage;
-    const uint32_t mask = __ballot_sync(0xffffffffu, live);
+    const uint32_t mask = __ballot_sync(0xffffffffu, prow != kNoRow);
     if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + Cfg::kMask), "r"(mask) : "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // keys g + 8 i
       const uint32_t r = __shfl_sync(0xffffffffu, prow, g + 8 * i);
-      const uint32_t bytes = r != 0xffffffffu ? 16u : 0u;
+      const uint32_t bytes = r != kNoRow ? 16u : 0u;
       const size_t o8 = bytes ? static_cast<size_t>(r) * D + t * 16 : 0;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -562,23 +566,25 @@ struct PgWarp {
     }
   }
 
-  // Run n tiles; raw(i) is this lane's key of tile i as a raw row (< 0:
-  // none), key0(i) the index of the tile's first key; before() runs once
-  // while the first copies are in flight (and makes qs ready).
+  // Run n tiles whose keys are found through the page table: raw(i) is this
+  // lane's key of tile i as a raw row (< 0: none), key0(i) the index of the
+  // tile's first key; before() runs once while the first copies are in flight
+  // (and makes qs ready).
   template <bool CAUSAL, typename RawFn, typename Key0Fn, typename BeforeFn>
   __device__ __forceinline__ void run(const PagedKV &kv, const int32_t *table, int kvh, int n, const Query &qs,
                                       RawFn raw, Key0Fn key0, const int (*lim)[2], uint32_t *status, BeforeFn before) {
     clear();
     int r = n > 0 ? raw(0) : -1;
     fetch(kv, table, r);
+    auto next = [&](int j, int st) {  // copy tile j, fetch the pages of tile j + 1
+      copy(kv, st, locate(kv, kvh, r >= 0, status));
+      r = j + 1 < n ? raw(j + 1) : -1;
+      fetch(kv, table, r);
+    };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
       if (i > 0 && i - 1 < n) put_scale(i - 1);
-      if (i < n) {
-        copy(kv, kvh, i, r >= 0, status);
-        r = i + 1 < n ? raw(i + 1) : -1;
-        fetch(kv, table, r);
-      }
+      if (i < n) next(i, i);
       cp_async_commit();
     }
     before();
@@ -588,16 +594,45 @@ struct PgWarp {
       if (j - 1 < n) put_scale(stc == 0 ? S - 1 : stc - 1);
       cp_async_wait<S - 2>();
       __syncwarp();
-      if (j < n) {
-        copy(kv, kvh, stc, r >= 0, status);
-        r = j + 1 < n ? raw(j + 1) : -1;
-        fetch(kv, table, r);
-      }
+      if (j < n) next(j, stc);
       cp_async_commit();
       step<CAUSAL>(qs, st, key0(i), lim);
       st = st == S - 1 ? 0 : st + 1;
       stc = stc == S - 1 ? 0 : stc + 1;
     }
+    finish();
+  }
+
+  // Run n tiles whose keys are known: row(i) gives this lane's key of tile i
+  // as a pool row (kNoRow: none) and puts its scales into sck, scv.
+  template <typename RowFn, typename BeforeFn>
+  __device__ __forceinline__ void run_known(const PagedKV &kv, int n, const Query &qs, RowFn row, BeforeFn before) {
+    clear();
+    auto next = [&](int j, int st) {
+      copy(kv, st, row(j));
+      put_scale(st);
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      if (i < n) next(i, i);
+      cp_async_commit();
+    }
+    before();
+    int st = 0, stc = S - 1;
+    for (int i = 0; i < n; ++i) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      if (i + S - 1 < n) next(i + S - 1, stc);
+      cp_async_commit();
+      step<false>(qs, st, 0, nullptr);
+      st = st == S - 1 ? 0 : st + 1;
+      stc = stc == S - 1 ? 0 : stc + 1;
+    }
+    finish();
+  }
+
+  // No copies in flight, the lanes' sums added up.
+  __device__ __forceinline__ void finish() {
     cp_async_wait<0>();
     __syncwarp();
 #pragma unroll
@@ -620,9 +655,8 @@ struct PgWarp {
 // to kPgWhole steps is not cut.  A segment inside one CTA is written
 // directly; of one that several CTAs share each leaves a partial record, which
 // k_paged_join adds up in CTA order.  (Joining by the last CTA to arrive took
-// 10 us of 108 at 4 x 128K rows, 4 query heads: one CTA, 28 records, one
-// dependent load behind the other; the second kernel has a warp a row and
-// takes 3.)  CTAs of 4 warps, 3 or 4 on an SM: one joins its warps while the
+// 10 us of 108 at 4 x 128K rows: 28 records of a segment, one dependent load
+// of a CTA's 4 warps behind the other.)  CTAs of 4 warps, 3 or 4 on an SM: one joins its warps while the
 // others stream.
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
@@ -876,29 +910,43 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
   if (tid == 0) a.joins[cta] = join;
 }
 
-// Grid (ctas, NT) behind k_paged_attend: CTA (c, nt) adds up 8 rows of the cut
-// segment that begins in c's part, a warp a row.  The records lie equally
-// spaced (c's own in slot 1, the others in slot 0); the first kBatch of them
-// are fetched while the weights (a record a lane) are made.
+// Grid (ctas, R / kRows) behind k_paged_attend: CTA (c, y) adds up kRows rows
+// of the cut segment that begins in c's part, kWarps warps a row.  The records
+// lie equally spaced (the first one's in slot 1, the others in slot 0); a
+// row's warps share them out (D / 4 lanes a record), the first kBatch of a lane
+// fetched while the weights (a record a lane, by every warp for itself) are
+// made.
+template <int D, int NT>
+struct PgJoin {
+  static constexpr int kWarps = D == 128 ? 4 : 1;  // 28 records of 128 dims at 4 x 128K rows, 6 of 64 at 16 x 32K
+  static constexpr int kRows = 8 / kWarps, kGridY = NT * kWarps;
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(256) k_paged_join(const PagedAttendArgs a) {
+  using J = PgJoin<D, NT>;
   constexpr int R = 8 * NT, kRec = D + kPartHeader, kStride = 2 * R * kRec;
-  constexpr int kSub = 128 / D, kBatch = 16;  // records side by side in a warp, and in flight a lane
-  extern __shared__ float cw[];               // [8][ctas] weights
+  constexpr int kSub = 128 / D, kBatch = 8, kEach = J::kWarps * kSub;  // records side by side in a row's warps
+  extern __shared__ float cw[];                                        // [8][ctas] weights
+  __shared__ float4 sums[8][32];
   pdl_wait();
-  const int4 join = __ldcg(a.joins + blockIdx.x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % J::kWarps;
+  const int r = J::kRows * blockIdx.y + warp / J::kWarps;
+  const int first = part * kSub + lane / (D / 4), d = 4 * (lane % (D / 4));
+  const int c0 = blockIdx.x;
+  const int4 join = __ldcg(a.joins + c0);
   if (join.x < 0) return;
-  const int kvh = join.y / a.rg, rg = join.y % a.rg;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = rg * R + 8 * blockIdx.y + warp;
-  if (x >= a.n_q * a.group) return;
-  const int nr = join.z - static_cast<int>(blockIdx.x) + 1, sub = lane / (D / 4), d = 4 * (lane % (D / 4));
-  const float *rec0 = a.part + static_cast<size_t>(blockIdx.x) * kStride + (8 * blockIdx.y + warp) * kRec;
+  const int kvh = join.y / a.rg, x = (join.y % a.rg) * R + r;
+  const bool on = x < a.n_q * a.group;  // (rows past the last: nothing to add)
+  const int nr = on ? join.z - c0 + 1 : 0;
+  const float *rec0 = a.part + static_cast<size_t>(c0) * kStride + r * kRec;
   auto rec_of = [&](int k) { return rec0 + (k == 0 ? R * kRec : static_cast<size_t>(k) * kStride); };
   float4 y[kBatch];
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int k = k0 + j * kSub + sub;
+      const int k = k0 + j * kEach + first;
+      y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k < nr) y[j] = __ldcg(reinterpret_cast<const float4 *>(rec_of(k) + kPartHeader + d));
     }
   };
@@ -918,25 +966,25 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedAttendArgs a) {
   for (int k = lane; k < nr; k += 32) w[k] = exp2_approx(w[k] - mm);
   __syncwarp();
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < nr; k0 += kBatch * kSub) {
+  for (int k0 = 0; k0 < nr; k0 += kBatch * kEach) {
     if (k0 > 0) fetch(k0);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int k = k0 + j * kSub + sub;
-      if (k < nr) {
-        const float c = w[k];
-        v = make_float4(fmaf(c, y[j].x, v.x), fmaf(c, y[j].y, v.y), fmaf(c, y[j].z, v.z), fmaf(c, y[j].w, v.w));
-      }
+      const int k = k0 + j * kEach + first;
+      const float c = k < nr ? w[k] : 0.f;
+      v = make_float4(fmaf(c, y[j].x, v.x), fmaf(c, y[j].y, v.y), fmaf(c, y[j].z, v.z), fmaf(c, y[j].w, v.w));
     }
   }
+  sums[warp][lane] = v;
+  __syncthreads();
+  if (on && part == 0 && lane < D / 4) {
 #pragma unroll
-  for (int o = D / 4; o < 32; o <<= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
-    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    for (int k = 1; k < kEach; ++k) {
+      const float4 u = sums[warp + k / kSub][lane + (k % kSub) * (D / 4)];
+      v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+    }
+    paged_put<D>(a, paged_row(a, join.x, kvh, x), d, v, mt, L);
   }
-  if (sub == 0) paged_put<D>(a, paged_row(a, join.x, kvh, x), d, v, mt, L);
 }
 
 // ------------------------------------------------------------------ unfolding
@@ -953,10 +1001,17 @@ struct PagedUnfoldArgs {
 
 constexpr int kPuWarps = kUnfoldWarps;
 
-// rings (over them, once drained, the warps' results) | queries | chunk ids | gist logits
+// rings (over them, once drained, the warps' results) | queries | items (the last one for the own chunk)
+struct PagedItem {
+  uint32_t prow;   // pool row of the chunk's first row, kNoRow: page outside the pool
+  float ks, vs;    // scales
+  int32_t id;      // chunk
+};
+
 template <int D, int FMT, bool QF32>
 __host__ __device__ inline size_t paged_unfold_smem(int per) {
-  return kPuWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, 1>) + static_cast<size_t>(per) * 8;
+  return kPuWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, 1>) +
+         (static_cast<size_t>(per) + 1) * (sizeof(PagedItem) + 4);
 }
 
 // The CTA's partial (its 2 kPuWarps states in red) goes to the row's split
@@ -1032,8 +1087,8 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
   extern __shared__ __align__(128) uint8_t smem[];
   const int per = (a.k + a.n_split - 1) / a.n_split;
   Query &qs = *reinterpret_cast<Query *>(smem + kPuWarps * PgCfg<D>::kRing);
-  int *items = reinterpret_cast<int *>(smem + kPuWarps * PgCfg<D>::kRing + sizeof(Query));
-  float *item_z = reinterpret_cast<float *>(items + per);
+  PagedItem *items = reinterpret_cast<PagedItem *>(smem + kPuWarps * PgCfg<D>::kRing + sizeof(Query));
+  float *item_z = reinterpret_cast<float *>(items + per + 1);  // gist logits (exclude mode)
   float(*red)[2 + D] = reinterpret_cast<float(*)[2 + D]>(smem);
   __shared__ int n_items_s, is_last_s, take_s[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -1065,15 +1120,34 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
   if (static_cast<int64_t>(N) * a.chunk + own > a.t_max) own = max(0, a.t_max - N * a.chunk);
   if (split != a.n_split - 1) own = 0;
 
-  // Selected chunks of this split, in list order (invalid entries dropped).
+  // Selected chunks of this split, in list order (invalid entries dropped), then the own chunk, each with its place
+  // in the pool (a chunk lies in one page).
+  const int32_t *table = kv.table + static_cast<size_t>(b) * kv.max_pages;
+  auto item = [&](int slot, int m) {
+    const int r = m * a.chunk, p = kv.page.div(r), off = r - p * static_cast<int>(kv.page.d);
+    const int pid = __ldcg(table + p);
+    PagedItem it = {Warp::kNoRow, 0.f, 0.f, m};
+    if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(kv.n_pages)) {
+      const uint32_t ph = static_cast<uint32_t>(pid) * kv.hkv + kvh;
+      const size_t si = static_cast<size_t>(ph) * kv.blocks + kv.chunk.div(off);
+      it.prow = ph * kv.page.d + off;
+      it.ks = __ldcg(kv.ks + si);
+      it.vs = __ldcg(kv.vs + si);
+    } else {
+      flag_error(a.status, GSA_DEVERR_BAD_INDEX);
+    }
+    items[slot] = it;
+  };
   const int i0 = min(a.k, split * per), i1 = min(a.k, i0 + per);
   if (warp == 0) {
     int cnt = 0;
     for (int base = i0; base < i1; base += 32) {
       const int i = base + lane;
       int m = -1;
+      float z = 0.f;
       if (i < i1) {
         m = __ldcg(a.sel_idx + row * a.k + i);
+        if (a.exclude) z = __ldcg(a.sel_score + row * a.k + i) * kLog2e;
         if (m >= N) {
           flag_error(a.status, GSA_DEVERR_BAD_INDEX);
           m = -1;
@@ -1082,34 +1156,39 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
       const unsigned ball = __ballot_sync(0xffffffffu, m >= 0);
       if (m >= 0) {
         const int slot = cnt + __popc(ball & ((1u << lane) - 1u));
-        items[slot] = m;
-        if (a.exclude) item_z[slot] = __ldcg(a.sel_score + row * a.k + i) * kLog2e;
+        item(slot, m);
+        item_z[slot] = z;
       }
       cnt += __popc(ball);
     }
-    if (lane == 0) n_items_s = cnt;
-  }
-  Warp w;
-  w.ring = smem_u32(smem) + warp * PgCfg<D>::kRing;
-  if (warp == 1)
+    if (lane == 0) {
+      n_items_s = cnt;
+      if (own > 0) item(cnt, N);
+    }
+  } else if (warp == 1) {
     qs.load(
         0,
         [&](int r) -> const void * {
           return r == 0 ? static_cast<const uint8_t *>(a.q) + row * D * (QF32 ? 4 : 2) : nullptr;
         },
         a.scale_log2);
+  }
+  Warp w;
+  w.ring = smem_u32(smem) + warp * PgCfg<D>::kRing;
   __syncthreads();
   const int n_sel = n_items_s, sel_rows = n_sel * a.chunk, n_keys = sel_rows + own;
   const int n_tiles = (n_keys + 31) >> 5;
   const int mine = n_tiles > warp ? (n_tiles - warp + kPuWarps - 1) / kPuWarps : 0;
-  auto key0 = [&](int i) { return (warp + kPuWarps * i) * 32; };
-  auto raw = [&](int i) {
-    const int j = key0(i) + lane;
-    if (j < sel_rows) {
-      const int it = kv.chunk.div(j);
-      return items[it] * a.chunk + (j - it * a.chunk);
-    }
-    return j < n_keys ? N * a.chunk + (j - sel_rows) : -1;
+  auto key = [&](int i) {
+    const int j = (warp + kPuWarps * i) * 32 + lane;
+    w.sck = w.scv = 0.f;
+    if (j >= n_keys) return Warp::kNoRow;
+    const int x = kv.chunk.div(j);
+    const PagedItem it = items[x];
+    if (it.prow == Warp::kNoRow) return Warp::kNoRow;
+    w.sck = it.ks;
+    w.scv = it.vs;
+    return it.prow + (j - x * a.chunk);
   };
   // gists of the selected chunks: D / 32 dims a lane
   constexpr int E = D / 32;
@@ -1122,7 +1201,7 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
 #pragma unroll 4
     for (int i = warp; i < n_sel; i += kPuWarps) {
       const float z = item_z[i];
-      const size_t at = (gv0 + items[i]) * D + E * lane;
+      const size_t at = (gv0 + items[i].id) * D + E * lane;
       float v[E];
       if (QF32) {
 #pragma unroll
@@ -1149,8 +1228,7 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
       for (int e = 0; e < E; ++e) ga[e] = fmaf(p, v[e], ga[e]);
     }
   };
-  w.template run<false>(kv, kv.table + static_cast<size_t>(b) * kv.max_pages, kvh, mine, qs, raw, key0, nullptr,
-                        a.status, gists);
+  w.run_known(kv, mine, qs, key, gists);
   pdl_trigger();
   __syncthreads();  // every ring is drained: red may overwrite them
   if (t == 0) {     // column 0

@@ -95,7 +95,8 @@ gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
   GSA_TRY(launch(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa));
   // no segment can have been cut when the longest is short
   if (pa.t_max <= static_cast<int>(kPgWhole) * kPgStep) return GSA_OK;
-  return launch(k_paged_join<D, NT>, dim3(grid, NT), dim3(256), static_cast<size_t>(grid) * 8 * 4, stream, pa);
+  return launch(k_paged_join<D, NT>, dim3(grid, PgJoin<D, NT>::kGridY), dim3(256), static_cast<size_t>(grid) * 8 * 4,
+                stream, pa);
 }
 
 gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q, const void *k, const void *v,
