@@ -36,6 +36,8 @@
 // scales one tile behind them.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "k_unfold.cuh"  // UnfoldArgs, ready list
 
@@ -604,25 +606,24 @@ struct PgWarp {
   }
 
   // Run n tiles whose keys are known: row(i) gives this lane's key of tile i
-  // as a pool row (kNoRow: none) and puts its scales into sck, scv.
+  // as a pool row (kNoRow: none) and fetches its scales into sck, scv.
   template <typename RowFn, typename BeforeFn>
   __device__ __forceinline__ void run_known(const PagedKV &kv, int n, const Query &qs, RowFn row, BeforeFn before) {
     clear();
-    auto next = [&](int j, int st) {
-      copy(kv, st, row(j));
-      put_scale(st);
-    };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
-      if (i < n) next(i, i);
+      if (i > 0 && i - 1 < n) put_scale(i - 1);
+      if (i < n) copy(kv, i, row(i));
       cp_async_commit();
     }
     before();
     int st = 0, stc = S - 1;
     for (int i = 0; i < n; ++i) {
+      const int j = i + S - 1;
+      if (j - 1 < n) put_scale(stc == 0 ? S - 1 : stc - 1);
       cp_async_wait<S - 2>();
       __syncwarp();
-      if (i + S - 1 < n) next(i + S - 1, stc);
+      if (j < n) copy(kv, stc, row(j));
       cp_async_commit();
       step<false>(qs, st, 0, nullptr);
       st = st == S - 1 ? 0 : st + 1;
@@ -1003,15 +1004,16 @@ constexpr int kPuWarps = kUnfoldWarps;
 
 // rings (over them, once drained, the warps' results) | queries | items (the last one for the own chunk)
 struct PagedItem {
-  uint32_t prow;   // pool row of the chunk's first row, kNoRow: page outside the pool
-  float ks, vs;    // scales
-  int32_t id;      // chunk
+  uint32_t prow;  // pool row of the chunk's first row, kNoRow: page outside the pool
+  uint32_t si;    // place of its scales
+  int32_t id;     // chunk
+  float z;        // logit of its gist (exclude mode)
 };
 
 template <int D, int FMT, bool QF32>
 __host__ __device__ inline size_t paged_unfold_smem(int per) {
   return kPuWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, 1>) +
-         (static_cast<size_t>(per) + 1) * (sizeof(PagedItem) + 4);
+         (static_cast<size_t>(per) + 1) * sizeof(PagedItem);
 }
 
 // The CTA's partial (its 2 kPuWarps states in red) goes to the row's split
@@ -1088,7 +1090,6 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
   const int per = (a.k + a.n_split - 1) / a.n_split;
   Query &qs = *reinterpret_cast<Query *>(smem + kPuWarps * PgCfg<D>::kRing);
   PagedItem *items = reinterpret_cast<PagedItem *>(smem + kPuWarps * PgCfg<D>::kRing + sizeof(Query));
-  float *item_z = reinterpret_cast<float *>(items + per + 1);  // gist logits (exclude mode)
   float(*red)[2 + D] = reinterpret_cast<float(*)[2 + D]>(smem);
   __shared__ int n_items_s, is_last_s, take_s[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -1115,6 +1116,14 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
   }
   const int kvh = h / a.group;
   const size_t row = static_cast<size_t>(b) * a.hq + h;
+  // the list's first entries, asked for together with the counts (one latency)
+  const int i0 = min(a.k, split * per), i1 = min(a.k, i0 + per);
+  int m0 = -1;
+  float z0 = 0.f;
+  if (warp == 0 && i0 + lane < i1) {
+    m0 = __ldcg(a.sel_idx + row * a.k + i0 + lane);
+    if (a.exclude) z0 = __ldcg(a.sel_score + row * a.k + i0 + lane);
+  }
   const int N = min(min(max(__ldcg(a.n_gists + b), 0), a.n_max), a.t_max / a.chunk);
   int own = min(max(__ldcg(a.own_len + b), 0), a.chunk);
   if (static_cast<int64_t>(N) * a.chunk + own > a.t_max) own = max(0, a.t_max - N * a.chunk);
@@ -1123,48 +1132,39 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
   // Selected chunks of this split, in list order (invalid entries dropped), then the own chunk, each with its place
   // in the pool (a chunk lies in one page).
   const int32_t *table = kv.table + static_cast<size_t>(b) * kv.max_pages;
-  auto item = [&](int slot, int m) {
+  auto item = [&](int slot, int m, float z) {
     const int r = m * a.chunk, p = kv.page.div(r), off = r - p * static_cast<int>(kv.page.d);
     const int pid = __ldcg(table + p);
-    PagedItem it = {Warp::kNoRow, 0.f, 0.f, m};
+    PagedItem it = {Warp::kNoRow, 0u, m, z};
     if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(kv.n_pages)) {
       const uint32_t ph = static_cast<uint32_t>(pid) * kv.hkv + kvh;
-      const size_t si = static_cast<size_t>(ph) * kv.blocks + kv.chunk.div(off);
       it.prow = ph * kv.page.d + off;
-      it.ks = __ldcg(kv.ks + si);
-      it.vs = __ldcg(kv.vs + si);
+      it.si = ph * kv.blocks + kv.chunk.div(off);
     } else {
       flag_error(a.status, GSA_DEVERR_BAD_INDEX);
     }
     items[slot] = it;
   };
-  const int i0 = min(a.k, split * per), i1 = min(a.k, i0 + per);
   if (warp == 0) {
     int cnt = 0;
     for (int base = i0; base < i1; base += 32) {
       const int i = base + lane;
-      int m = -1;
-      float z = 0.f;
-      if (i < i1) {
+      int m = m0;
+      float z = z0;
+      if (base > i0 && i < i1) {
         m = __ldcg(a.sel_idx + row * a.k + i);
-        if (a.exclude) z = __ldcg(a.sel_score + row * a.k + i) * kLog2e;
-        if (m >= N) {
-          flag_error(a.status, GSA_DEVERR_BAD_INDEX);
-          m = -1;
-        }
+        if (a.exclude) z = __ldcg(a.sel_score + row * a.k + i);
+      }
+      if (i >= i1) m = -1;
+      if (m >= N) {
+        flag_error(a.status, GSA_DEVERR_BAD_INDEX);
+        m = -1;
       }
       const unsigned ball = __ballot_sync(0xffffffffu, m >= 0);
-      if (m >= 0) {
-        const int slot = cnt + __popc(ball & ((1u << lane) - 1u));
-        item(slot, m);
-        item_z[slot] = z;
-      }
+      if (m >= 0) item(cnt + __popc(ball & ((1u << lane) - 1u)), m, z * kLog2e);
       cnt += __popc(ball);
     }
-    if (lane == 0) {
-      n_items_s = cnt;
-      if (own > 0) item(cnt, N);
-    }
+    if (lane == 0) n_items_s = cnt;
   } else if (warp == 1) {
     qs.load(
         0,
@@ -1172,6 +1172,8 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
           return r == 0 ? static_cast<const uint8_t *>(a.q) + row * D * (QF32 ? 4 : 2) : nullptr;
         },
         a.scale_log2);
+  } else if (warp == 2 && lane == 0 && own > 0) {
+    item(per, N, 0.f);  // the own chunk has the last place
   }
   Warp w;
   w.ring = smem_u32(smem) + warp * PgCfg<D>::kRing;
@@ -1184,48 +1186,46 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
     w.sck = w.scv = 0.f;
     if (j >= n_keys) return Warp::kNoRow;
     const int x = kv.chunk.div(j);
-    const PagedItem it = items[x];
-    if (it.prow == Warp::kNoRow) return Warp::kNoRow;
-    w.sck = it.ks;
-    w.scv = it.vs;
-    return it.prow + (j - x * a.chunk);
+    const uint2 it = *reinterpret_cast<const uint2 *>(&items[x < n_sel ? x : per]);  // prow, si
+    if (it.x == Warp::kNoRow) return Warp::kNoRow;
+    w.sck = __ldcg(kv.ks + it.y);
+    w.scv = __ldcg(kv.vs + it.y);
+    return it.x + (j - x * a.chunk);
   };
-  // gists of the selected chunks: D / 32 dims a lane
-  constexpr int E = D / 32;
+  // gists of the selected chunks, relative to their own largest logit: kLpr lanes a row (16 bytes each), kRows rows a
+  // warp at once, 8 such loads in flight a lane (one row behind the other took 5 us of 16 at 64 gists)
+  using T = typename std::conditional<QF32, float, __nv_bfloat16>::type;
+  constexpr int E = Vec16<T>::kElems, kLpr = D / E, kRows = 32 / kLpr;
   float gm = neg_inf(), gl = 0.f, ga[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) ga[e] = 0.f;
   auto gists = [&] {
     if (!a.exclude) return;
-    const size_t gv0 = (static_cast<size_t>(b) * a.hkv + kvh) * a.n_max;
-#pragma unroll 4
-    for (int i = warp; i < n_sel; i += kPuWarps) {
-      const float z = item_z[i];
-      const size_t at = (gv0 + items[i].id) * D + E * lane;
-      float v[E];
-      if (QF32) {
+    for (int i = lane; i < n_sel; i += 32) gm = fmaxf(gm, items[i].z);
+    gm = warp_max(gm);
+    const float ref = gm == neg_inf() ? 0.f : gm;
+    const T *gv = static_cast<const T *>(a.gist_v) + (static_cast<size_t>(b) * a.hkv + kvh) * a.n_max * D +
+                  E * (lane % kLpr);
+    for (int i0 = warp * kRows + lane / kLpr; i0 < n_sel; i0 += 8 * kPuWarps * kRows) {
+      uint4 v[8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = __ldcg(static_cast<const float *>(a.gist_v) + at + e);
-      } else {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.gist_v) + at);
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * kPuWarps * kRows;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (i < n_sel) v[j] = __ldcg(reinterpret_cast<const uint4 *>(gv + static_cast<size_t>(items[i].id) * D));
+      }
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          const uint32_t x = __ldcg(p + e);
-          v[2 * e] = bf16_lo(x);
-          v[2 * e + 1] = bf16_hi(x);
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * kPuWarps * kRows;
+        if (i < n_sel) {
+          const float p = exp2_approx(items[i].z - ref);
+          float x[E];
+          Vec16<T>::unpack(v[j], x);
+          gl += p;
+#pragma unroll
+          for (int e = 0; e < E; ++e) ga[e] = fmaf(p, x[e], ga[e]);
         }
       }
-      if (z > gm + kRescaleSlack) {
-        const float c = exp2_approx(gm - z);
-        gl *= c;
-#pragma unroll
-        for (int e = 0; e < E; ++e) ga[e] *= c;
-        gm = z;
-      }
-      const float p = exp2_approx(z - (gm == neg_inf() ? 0.f : gm));
-      gl += p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) ga[e] = fmaf(p, v[e], ga[e]);
     }
   };
   w.run_known(kv, mine, qs, key, gists);
@@ -1243,10 +1243,18 @@ __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
     }
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) red[kPuWarps + warp][2 + E * lane + e] = ga[e];
-  if (lane == 0) {
-    red[kPuWarps + warp][0] = gm;
-    red[kPuWarps + warp][1] = gl;
+  for (int o = kLpr; o < 32; o <<= 1) {
+    gl += __shfl_xor_sync(0xffffffffu, gl, o);
+#pragma unroll
+    for (int e = 0; e < E; ++e) ga[e] += __shfl_xor_sync(0xffffffffu, ga[e], o);
+  }
+  if (lane < kLpr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[kPuWarps + warp][2 + E * lane + e] = ga[e];
+    if (lane == 0) {
+      red[kPuWarps + warp][0] = gm;
+      red[kPuWarps + warp][1] = gl;
+    }
   }
   paged_unfold_finish<D>(a, row, split, red, is_last_s);
   if (a.ready.w) unfold_ready_done(a);
