@@ -18,7 +18,13 @@
 // launch and three dependent loads for single tokens.  A CTA takes one block
 // of one sequence for all heads (or a share of the heads when there are few
 // blocks), so the sines of a row are computed once and every block of codes
-// has one writer; a warp takes one (block, head) at a time, 8 dims a lane.
+// has one writer; a warp takes one (block, head) of keys or
+// values, or one row's queries of a few heads, at a time.  A lane works on a
+// unit of 16 dims, the 8 pairs that turn together, so nothing is loaded twice,
+// and a block of up to kHold passes of rows is held in registers between its
+// maximum and its codes.  (32768 tokens, 32 / 8 heads of 64 dims, e4m3: 127 us
+// with 8 dims a lane, each lane loading its partner's too and an index division
+// a row.)
 #pragma once
 
 #include <cuda_fp8.h>
@@ -43,7 +49,7 @@ struct AppendArgs {
   void *q_out;                 // [n_tok, hq, D]
   int64_t q_stride, k_stride, v_stride;
   int32_t n_tok, B, hq, hkv, n_max, t_max, n_pages, max_pages, blocks;
-  int32_t rot, inter, advance;
+  int32_t rot, advance;
   FastDiv page, chunk;
   uint32_t *counter, *status;
 };
@@ -72,17 +78,72 @@ __device__ __forceinline__ int append_span(const AppendArgs &a, int b, int &star
   return n;
 }
 
-// Eight elements of T at p as floats.
+// A unit of 16 dims of a row as it lies in memory: dims A .. A + 7 and B ..
+// B + 7 (see unit_dims).
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float *x) {
-  if (sizeof(T) == 2) {
-    Vec16<__nv_bfloat16>::unpack(ldg_nc_v4(p), x);
-  } else {
-    Vec16<float>::unpack(ldg_nc_v4(p), x);
-    Vec16<float>::unpack(ldg_nc_v4(reinterpret_cast<const float *>(p) + 4), x + 4);
+struct Raw16 {
+  static constexpr int kVecs = sizeof(T) / 2;  // 16-byte loads of 8 dims
+  uint4 a[kVecs], b[kVecs];
+  __device__ __forceinline__ void load(const T *row, int A, int B) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      a[i] = ldg_nc_v4(row + A + i * 4);
+      b[i] = ldg_nc_v4(row + B + i * 4);
+    }
   }
+  __device__ __forceinline__ void values(float *x) const {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      Vec16<T>::unpack(a[i], x + i * 4);
+      Vec16<T>::unpack(b[i], x + 8 + i * 4);
+    }
+  }
+};
+
+// Dims of unit i: pairs of halves: 8 i and rot / 2 + 8 i; interleaved pairs,
+// and dims that are not turned: 16 i and 16 i + 8.
+template <bool INTER>
+__device__ __forceinline__ void unit_dims(int i, int rot, int &A, int &B) {
+  const bool halves = !INTER && i < (rot >> 4);
+  A = halves ? 8 * i : 16 * i;
+  B = halves ? (rot >> 1) + 8 * i : 16 * i + 8;
 }
 
+// The unit's 8 (cos, sin), (1, 0) for dims that are not turned.
+struct Turn8 {
+  float4 c[4];
+  __device__ __forceinline__ void load(const float2 *row, int i, int rot) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      c[k] = i < (rot >> 4) ? reinterpret_cast<const float4 *>(row + 8 * i)[k] : make_float4(1.f, 0.f, 1.f, 0.f);
+  }
+  // x[0..7] dims A.., x[8..15] dims B..
+  template <bool INTER>
+  __device__ __forceinline__ void turn(float *x) const {
+    if (INTER) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pair(k, x[2 * k], x[2 * k + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pair(k, x[k], x[8 + k]);
+    }
+  }
+  __device__ __forceinline__ void pair(int k, float &u, float &v) const {
+    const float cs = k & 1 ? c[k / 2].z : c[k / 2].x, sn = k & 1 ? c[k / 2].w : c[k / 2].y;
+    const float p = fmaf(u, cs, -(v * sn));
+    v = fmaf(v, cs, u * sn);
+    u = p;
+  }
+};
+
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight values to T at p.
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float *x) {
   if (sizeof(T) == 2) {
@@ -98,36 +159,6 @@ __device__ __forceinline__ void store8(T *p, const float *x) {
     float4 *f = reinterpret_cast<float4 *>(p);
     f[0] = make_float4(x[0], x[1], x[2], x[3]);
     f[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-}
-
-// Dims e .. e + 7 of the row at p, turned by the row's table of (cos, sin).
-// Halves: dim i pairs with i + rot / 2; interleaved: 2 i with 2 i + 1.  rot
-// is a multiple of 16, so the 8 dims lie in one half, and so do their
-// partners.
-template <typename T>
-__device__ __forceinline__ void load_turned(const T *p, int e, int rot, int inter, const float2 *cs, float *x) {
-  load8(p + e, x);
-  if (e >= rot) return;
-  if (inter) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 c = cs[e / 2 + i];
-      const float u = x[2 * i], v = x[2 * i + 1];
-      x[2 * i] = fmaf(u, c.x, -(v * c.y));
-      x[2 * i + 1] = fmaf(v, c.x, u * c.y);
-    }
-  } else {
-    const int half = rot >> 1;
-    const bool up = e >= half;
-    const int f = up ? e - half : e;
-    float y[8];
-    load8(p + (up ? f : e + half), y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 c = cs[f + i];
-      x[i] = fmaf(x[i], c.x, up ? y[i] * c.y : -(y[i] * c.y));
-    }
   }
 }
 
@@ -183,67 +214,127 @@ __device__ __forceinline__ void decode8(uint2 c, float *x) {
 // One (block, kv head) of keys (TURN) or values: n new rows from token row
 // `src` on (stride elements apart) go to page row `dst`.., `held` rows of the
 // block come before them.
-template <int D, typename T, int FMT, bool TURN>
+template <int D, typename T, int FMT, bool INTER, bool TURN>
 __device__ __forceinline__ void append_block(const T *src, int64_t stride, int n, int held, void *pages, size_t dst,
-                                             float *scale, int rot, int inter, const float2 *cs) {
-  constexpr int L = D / 8, RPW = 32 / L;  // lanes of a row, rows of a pass
-  const int lane = threadIdx.x & 31, sub = lane / L, e = 8 * (lane % L);
-  float x[8];
-  auto load = [&](int r) {
-    if (TURN)
-      load_turned(src + r * stride, e, rot, inter, cs + r * (rot / 2), x);
-    else
-      load8(src + r * stride + e, x);
+                                             float *scale, int rot, const float2 *cs) {
+  constexpr int L = D / 16, RPW = 32 / L;        // lanes of a row, rows of a pass
+  constexpr int kHold = 1;                       // passes held in registers
+  const int lane = threadIdx.x & 31, sub = lane / L, unit = lane % L;
+  int A, B;
+  unit_dims<INTER>(unit, rot, A, B);
+  auto turned = [&](const Raw16<T> &raw, int r, float *x) {
+    raw.values(x);
+    if (TURN && rot) {
+      Turn8 t;
+      t.load(cs + r * (rot / 2), unit, rot);
+      t.turn<INTER>(x);
+    }
   };
   if (FMT == kFmtPlain) {
     T *out = static_cast<T *>(pages) + dst * D;
 #pragma unroll 2
     for (int r = sub; r < n; r += RPW) {
-      load(r);
-      store8(out + static_cast<size_t>(r) * D + e, x);
+      Raw16<T> raw;
+      raw.load(src + r * stride, A, B);
+      float x[16];
+      turned(raw, r, x);
+      store8(out + static_cast<size_t>(r) * D + A, x);
+      store8(out + static_cast<size_t>(r) * D + B, x + 8);
     }
     return;
   }
   constexpr int F = FMT == kFmtPlain ? kFmtI8 : FMT;  // (the plain case has returned)
-  uint32_t amax = 0;
-#pragma unroll 2
-  for (int r = sub; r < n; r += RPW) {
-    load(r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-  }
-  amax = __reduce_max_sync(0xffffffffu, amax);
   const float old = held > 0 ? __ldcg(scale) : 0.f;
+  float x[kHold][16], top = 0.f;
+  // rows r0 + sub + RPW i of this lane, turned
+  auto fetch = [&](int r0) {
+    Raw16<T> raw[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * RPW + sub < n) raw[i].load(src + (r0 + i * RPW + sub) * stride, A, B);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * RPW + sub < n) turned(raw[i], r0 + i * RPW + sub, x[i]);
+  };
+#pragma unroll 1
+  for (int r0 = 0; r0 < n; r0 += kHold * RPW) {
+    fetch(r0);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * RPW + sub < n) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = max_nan(top, fabsf(x[i][k]));
+      }
+  }
+  const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // (a NaN has the largest bits)
   float s = block_scale<F>(amax);
   if (!(s > old) && s == s) s = old;  // the larger; NaN from either stays
   uint8_t *out = static_cast<uint8_t *>(pages) + dst * D;
-  if (s > old && held > 0) {
+  if (s > old && held > 0) {  // the rows already there, at the new scale
     const float ratio = old / s;
     uint8_t *first = out - static_cast<size_t>(held) * D;
     for (int r = sub; r < held; r += RPW) {
-      uint2 *p = reinterpret_cast<uint2 *>(first + static_cast<size_t>(r) * D + e);
-      float y[8];
-      decode8<F>(__ldcg(p), y);
-      *p = encode8<F>(y, ratio);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2 *p = reinterpret_cast<uint2 *>(first + static_cast<size_t>(r) * D + (h ? B : A));
+        float y[8];
+        decode8<F>(__ldcg(p), y);
+        *p = encode8<F>(y, ratio);
+      }
     }
   }
   const float inv = s > 0.f ? __frcp_rn(s) : 0.f;  // 0 for a scale of 0 or NaN: codes 0
-#pragma unroll 2
-  for (int r = sub; r < n; r += RPW) {
-    load(r);
-    uint2 c = make_uint2(0, 0);
-    if (inv > 0.f) c = encode8<F>(x, inv);
-    *reinterpret_cast<uint2 *>(out + static_cast<size_t>(r) * D + e) = c;
+#pragma unroll 1
+  for (int r0 = 0; r0 < n; r0 += kHold * RPW) {
+    if (n > kHold * RPW) fetch(r0);  // not held: read again
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int r = r0 + i * RPW + sub;
+      if (r < n) {
+        uint2 c = make_uint2(0, 0), d = make_uint2(0, 0);
+        if (inv > 0.f) {
+          c = encode8<F>(x[i], inv);
+          d = encode8<F>(x[i] + 8, inv);
+        }
+        *reinterpret_cast<uint2 *>(out + static_cast<size_t>(r) * D + A) = c;
+        *reinterpret_cast<uint2 *>(out + static_cast<size_t>(r) * D + B) = d;
+      }
+    }
   }
   __syncwarp();
   if (lane == 0) *scale = s;
 }
 
+// kQPass passes of RPW heads of one row's queries, from head h0 on.
+constexpr int kQPass = 2;
+template <int D, typename T, bool INTER>
+__device__ __forceinline__ void append_queries(const T *q, T *out, int h0, int hq, int rot, const float2 *cs) {
+  constexpr int L = D / 16, RPW = 32 / L;
+  const int lane = threadIdx.x & 31, h = h0 + lane / L, unit = lane % L;
+  int A, B;
+  unit_dims<INTER>(unit, rot, A, B);
+  Raw16<T> raw[kQPass];
+#pragma unroll
+  for (int i = 0; i < kQPass; ++i)
+    if (h + i * RPW < hq) raw[i].load(q + (h + i * RPW) * D, A, B);
+  Turn8 t;
+  t.load(cs, unit, rot);
+#pragma unroll
+  for (int i = 0; i < kQPass; ++i)
+    if (h + i * RPW < hq) {
+      float x[16];
+      raw[i].values(x);
+      t.turn<INTER>(x);
+      store8(out + (h + i * RPW) * D + A, x);
+      store8(out + (h + i * RPW) * D + B, x + 8);
+    }
+}
+
 // Grid (x, y): CTA x takes blocks x, x + gridDim.x, .. of the line of all
 // sequences' touched blocks; the y CTAs share a block's heads.
-template <int D, typename T, int FMT>
-__global__ void __launch_bounds__(kApThreads, 4) k_paged_append(const AppendArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+template <int D, typename T, int FMT, bool INTER>
+__global__ void __launch_bounds__(kApThreads, 3) k_paged_append(const AppendArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
   float2 *cs = reinterpret_cast<float2 *>(smem);  // [chunk][rot / 2]
   uint32_t *pre = reinterpret_cast<uint32_t *>(cs + a.chunk.d * (a.rot / 2));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -255,23 +346,39 @@ __global__ void __launch_bounds__(kApThreads, 4) k_paged_append(const AppendArgs
     return n > 0 ? a.chunk.div(start + n - 1) - a.chunk.div(start) + 1 : 0u;
   });
   const uint32_t total = pre[a.B];
-  constexpr int L = D / 8, RPW = 32 / L;
-  for (uint32_t u = blockIdx.x; u < total; u += gridDim.x) {
+  // what a block is and where it goes; warp 0 works out the next one's while the others are at their tasks
+  struct Unit {
+    int tok, r0, rows, held, pid, off;
+  };
+  __shared__ Unit units[2];
+  auto prepare = [&](uint32_t u, Unit &out) {
+    if (u >= total) return;
     const int b = paged_find(pre, a.B, u);
     int start, tok0;
     const int n = append_span(a, b, start, tok0);
     const int blk = a.chunk.div(start) + (u - pre[b]);
-    const int r0 = max(start, blk * chunk), r1 = min(start + n, (blk + 1) * chunk);  // t_max <= 2^28
-    const int rows = r1 - r0, held = r0 - blk * chunk;
-    const int64_t tok = tok0 + (r0 - start);
-    const uint32_t pg = a.page.div(r0);
-    const int pid = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + pg);
+    Unit x;
+    x.r0 = max(start, blk * chunk);
+    x.rows = min(start + n, (blk + 1) * chunk) - x.r0;  // (t_max <= 2^28)
+    x.held = x.r0 - blk * chunk;
+    x.tok = tok0 + (x.r0 - start);
+    const uint32_t pg = a.page.div(x.r0);
+    x.pid = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + pg);
+    x.off = x.r0 - static_cast<int>(pg) * static_cast<int>(a.page.d);
+    if (lane == 0) out = x;
+  };
+  if (warp == 0) prepare(blockIdx.x, units[0]);
+  __syncthreads();
+  int flip = 0;
+  for (uint32_t u = blockIdx.x; u < total; u += gridDim.x, flip ^= 1) {
+    const Unit x = units[flip];
+    const int rows = x.rows, held = x.held, pid = x.pid, off = x.off;
+    const int64_t tok = x.tok;
     const bool live = static_cast<uint32_t>(pid) < static_cast<uint32_t>(a.n_pages);
     if (!live && tid == 0) flag_error(a.status, GSA_DEVERR_BAD_INDEX);
-    const int off = r0 - static_cast<int>(pg) * static_cast<int>(a.page.d);
     for (int i = tid; i < rows * half; i += kApThreads) {
       const int r = i / half, f = i - r * half;
-      const int p = a.pos ? __ldcg(a.pos + tok + r) : r0 + r;
+      const int p = a.pos ? __ldcg(a.pos + tok + r) : x.r0 + r;
       // turns in 64 bits; the fraction of a turn as fp32 plus its remainder
       const double turns = static_cast<double>(p) * static_cast<double>(__ldcg(a.inv_freq + f)) * 0.15915494309189535;
       const double fr = 2.0 * (turns - rint(turns));
@@ -282,10 +389,12 @@ __global__ void __launch_bounds__(kApThreads, 4) k_paged_append(const AppendArgs
       cs[i] = make_float2(fmaf(-lo, sn, cn), fmaf(lo, cn, sn));
     }
     __syncthreads();
-    // tasks: K and V of each kv head, then the queries' rows in passes of RPW
+    if (warp == 0) prepare(u + gridDim.x, units[flip ^ 1]);
+    // tasks: K and V of each kv head, then the rows' queries in groups of kQPass passes
+    constexpr int kHeads = kQPass * 32 / (D / 16);  // heads of a group
     const int kv_tasks = live ? 2 * a.hkv : 0;
-    const int q_rows = a.q ? rows * a.hq : 0;
-    const int tasks = kv_tasks + (q_rows + 2 * RPW - 1) / (2 * RPW);
+    const int groups = a.q ? (a.hq + kHeads - 1) / kHeads : 0;
+    const int tasks = kv_tasks + rows * groups;
     for (int i = blockIdx.y * kApWarps + warp; i < tasks; i += gridDim.y * kApWarps) {
       if (i < kv_tasks) {
         const bool is_v = i >= a.hkv;
@@ -293,27 +402,19 @@ __global__ void __launch_bounds__(kApThreads, 4) k_paged_append(const AppendArgs
         const size_t ph = static_cast<size_t>(pid) * a.hkv + h;
         const size_t dst = ph * a.page.d + off, si = ph * a.blocks + a.chunk.div(off);
         if (is_v)
-          append_block<D, T, FMT, false>(static_cast<const T *>(a.v) + tok * a.v_stride + static_cast<size_t>(h) * D,
-                                         a.v_stride, rows, held, a.vp, dst, a.vs + si, 0, 0, nullptr);
+          append_block<D, T, FMT, INTER, false>(static_cast<const T *>(a.v) + tok * a.v_stride + static_cast<size_t>(h) * D,
+                                         a.v_stride, rows, held, a.vp, dst, a.vs + si, 0, nullptr);
         else
-          append_block<D, T, FMT, true>(static_cast<const T *>(a.k) + tok * a.k_stride + static_cast<size_t>(h) * D,
-                                        a.k_stride, rows, held, a.kp, dst, a.ks + si, a.rot, a.inter, cs);
+          append_block<D, T, FMT, INTER, true>(static_cast<const T *>(a.k) + tok * a.k_stride + static_cast<size_t>(h) * D,
+                                        a.k_stride, rows, held, a.kp, dst, a.ks + si, a.rot, cs);
       } else {
-        const int e = 8 * (lane % L);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int j = ((i - kv_tasks) * 2 + x) * RPW + lane / L;
-          if (j < q_rows) {
-            const int r = j / a.hq, h = j - r * a.hq;
-            float y[8];
-            load_turned(static_cast<const T *>(a.q) + (tok + r) * a.q_stride + static_cast<size_t>(h) * D, e, a.rot,
-                        a.inter, cs + r * half, y);
-            store8(static_cast<T *>(a.q_out) + (static_cast<size_t>(tok + r) * a.hq + h) * D + e, y);
-          }
-        }
+        const int r = (i - kv_tasks) / groups, grp = (i - kv_tasks) - r * groups;
+        append_queries<D, T, INTER>(static_cast<const T *>(a.q) + (tok + r) * a.q_stride,
+                             static_cast<T *>(a.q_out) + (tok + r) * static_cast<int64_t>(a.hq) * D, grp * kHeads, a.hq,
+                             a.rot, cs + r * half);
       }
     }
-    __syncthreads();  // the table of sines is read
+    __syncthreads();  // the table of sines is read, the next unit is there
   }
   pdl_trigger();
   if (a.advance) {

@@ -149,19 +149,19 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
   });
 }
 
-template <int D, typename T, int FMT>
+template <int D, typename T, int FMT, bool INTER>
 gsa_status launch_append(const AppendArgs &aa, void *stream) {
   // an upper bound of the touched blocks: a sequence's first and last one may be part-filled
   const int chunk = static_cast<int>(aa.chunk.d);
   const int64_t most = std::min<int64_t>(aa.n_tok, aa.n_tok / chunk + 2 * static_cast<int64_t>(aa.B));
   const size_t smem = static_cast<size_t>(chunk) * (aa.rot / 2) * 8 + (static_cast<size_t>(aa.B) + 1) * 4;
-  const auto kern = k_paged_append<D, T, FMT>;
+  const auto kern = k_paged_append<D, T, FMT, INTER>;
   static SlotCache cache;
   const int slots = cache.get(kern, kApThreads, smem);
   const int x = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, slots)));
   // few blocks: several CTAs share the heads of each, one task a warp
   const int rows = static_cast<int>((aa.n_tok + most - 1) / most);
-  const int tasks = 2 * aa.hkv + (aa.q ? cdiv(rows * aa.hq, 2 * 32 / (D / 8)) : 0);
+  const int tasks = 2 * aa.hkv + (aa.q ? rows * cdiv(aa.hq, kQPass * 32 / (D / 16)) : 0);
   const int y = clampi(slots / x, 1, cdiv(tasks, kApWarps));
   return launch(kern, dim3(x, y), dim3(kApThreads), smem, stream, aa);
 }
@@ -241,22 +241,24 @@ gsa_status gsa_paged_append(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
   aa.max_pages = pdesc->max_pages;
   aa.blocks = pdesc->page / desc->chunk;
   aa.rot = adesc->rot_dim;
-  aa.inter = adesc->interleaved;
   aa.advance = adesc->advance;
   aa.page.init(pdesc->page);
   aa.chunk.init(desc->chunk);
   aa.counter = reinterpret_cast<uint32_t *>(at(ws, L.pg_append));
   aa.status = reinterpret_cast<uint32_t *>(at(ws, L.status));
-  const bool d64 = desc->d == 64;
-  auto go = [&](auto type) {
+  auto go = [&](auto type, auto inter) {
     using T = decltype(type);
+    constexpr bool I = decltype(inter)::value;
+    const bool d64 = desc->d == 64;
     if (pdesc->cache_dtype == GSA_I8)
-      return d64 ? launch_append<64, T, kFmtI8>(aa, stream) : launch_append<128, T, kFmtI8>(aa, stream);
+      return d64 ? launch_append<64, T, kFmtI8, I>(aa, stream) : launch_append<128, T, kFmtI8, I>(aa, stream);
     if (pdesc->cache_dtype == GSA_E4M3)
-      return d64 ? launch_append<64, T, kFmtE4M3>(aa, stream) : launch_append<128, T, kFmtE4M3>(aa, stream);
-    return d64 ? launch_append<64, T, kFmtPlain>(aa, stream) : launch_append<128, T, kFmtPlain>(aa, stream);
+      return d64 ? launch_append<64, T, kFmtE4M3, I>(aa, stream) : launch_append<128, T, kFmtE4M3, I>(aa, stream);
+    return d64 ? launch_append<64, T, kFmtPlain, I>(aa, stream) : launch_append<128, T, kFmtPlain, I>(aa, stream);
   };
-  return desc->dtype == GSA_BF16 ? go(__nv_bfloat16()) : go(0.f);
+  if (desc->dtype == GSA_BF16)
+    return adesc->interleaved ? go(__nv_bfloat16(), std::true_type()) : go(__nv_bfloat16(), std::false_type());
+  return adesc->interleaved ? go(0.f, std::true_type()) : go(0.f, std::false_type());
 }
 
 gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_t n_q, const void *q,
