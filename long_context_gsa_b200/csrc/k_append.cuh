@@ -18,13 +18,14 @@
 // launch and three dependent loads for single tokens.  A CTA takes one block
 // of one sequence for all heads (or a share of the heads when there are few
 // blocks), so the sines of a row are computed once and every block of codes
-// has one writer; a warp takes one (block, head) of keys or
-// values, or one row's queries of a few heads, at a time.  A lane works on a
-// unit of 16 dims, the 8 pairs that turn together, so nothing is loaded twice,
-// and a block of up to kHold passes of rows is held in registers between its
-// maximum and its codes.  (32768 tokens, 32 / 8 heads of 64 dims, e4m3: 127 us
-// with 8 dims a lane, each lane loading its partner's too and an index division
-// a row.)
+// has one writer; a warp takes one (block, head) of keys or values, or one
+// row's queries of a few heads, at a time.  A lane works on a unit of 16 dims,
+// the 8 pairs that turn together, so nothing is loaded twice, and a block of
+// up to kHold passes of rows stays in registers between its maximum and its
+// codes.  32768 tokens, 32 / 8 heads of 64 dims, e4m3 (369 MB): 127 us with 8
+// dims a lane, each lane loading its partner's too and an index division a
+// row; 86 us so (4.3 TB/s).  CTAs of 128 threads, 5 on an SM: 256 threads took
+// 87..94 us, 64 threads as long; more queries in flight a lane spill.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -47,14 +48,14 @@ struct AppendArgs {
   void *kp, *vp;               // pages
   float *ks, *vs;              // scales (8-bit)
   void *q_out;                 // [n_tok, hq, D]
-  int64_t q_stride, k_stride, v_stride;
+  int32_t q_stride, k_stride, v_stride;
   int32_t n_tok, B, hq, hkv, n_max, t_max, n_pages, max_pages, blocks;
   int32_t rot, advance;
   FastDiv page, chunk;
   uint32_t *counter, *status;
 };
 
-constexpr int kApThreads = 256;
+constexpr int kApThreads = 128;
 constexpr int kApWarps = kApThreads / 32;
 
 // First new raw row and number of new rows of sequence b, cut at t_max.
@@ -109,13 +110,14 @@ __device__ __forceinline__ void unit_dims(int i, int rot, int &A, int &B) {
   B = halves ? (rot >> 1) + 8 * i : 16 * i + 8;
 }
 
-// The unit's 8 (cos, sin), (1, 0) for dims that are not turned.
+// The unit's 8 (cos, sin); for dims that are not turned the 8 times (1, 0)
+// that the table begins with (its rows of rot / 2 follow).
 struct Turn8 {
   float4 c[4];
-  __device__ __forceinline__ void load(const float2 *row, int i, int rot) {
+  __device__ __forceinline__ void load(const float2 *cs, int r, int i, int rot) {
+    const float4 *p = reinterpret_cast<const float4 *>(i < (rot >> 4) ? cs + 8 + r * (rot >> 1) + 8 * i : cs);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      c[k] = i < (rot >> 4) ? reinterpret_cast<const float4 *>(row + 8 * i)[k] : make_float4(1.f, 0.f, 1.f, 0.f);
+    for (int k = 0; k < 4; ++k) c[k] = p[k];
   }
   // x[0..7] dims A.., x[8..15] dims B..
   template <bool INTER>
@@ -215,7 +217,7 @@ __device__ __forceinline__ void decode8(uint2 c, float *x) {
 // `src` on (stride elements apart) go to page row `dst`.., `held` rows of the
 // block come before them.
 template <int D, typename T, int FMT, bool INTER, bool TURN>
-__device__ __forceinline__ void append_block(const T *src, int64_t stride, int n, int held, void *pages, size_t dst,
+__device__ __forceinline__ void append_block(const T *src, int stride, int n, int held, void *pages, uint32_t dst,
                                              float *scale, int rot, const float2 *cs) {
   constexpr int L = D / 16, RPW = 32 / L;        // lanes of a row, rows of a pass
   constexpr int kHold = 1;                       // passes held in registers
@@ -224,22 +226,22 @@ __device__ __forceinline__ void append_block(const T *src, int64_t stride, int n
   unit_dims<INTER>(unit, rot, A, B);
   auto turned = [&](const Raw16<T> &raw, int r, float *x) {
     raw.values(x);
-    if (TURN && rot) {
+    if (TURN) {
       Turn8 t;
-      t.load(cs + r * (rot / 2), unit, rot);
+      t.load(cs, r, unit, rot);
       t.turn<INTER>(x);
     }
   };
   if (FMT == kFmtPlain) {
-    T *out = static_cast<T *>(pages) + dst * D;
+    T *out = static_cast<T *>(pages) + static_cast<size_t>(dst) * D;
 #pragma unroll 2
     for (int r = sub; r < n; r += RPW) {
       Raw16<T> raw;
-      raw.load(src + r * stride, A, B);
+      raw.load(src + static_cast<int64_t>(r) * stride, A, B);
       float x[16];
       turned(raw, r, x);
-      store8(out + static_cast<size_t>(r) * D + A, x);
-      store8(out + static_cast<size_t>(r) * D + B, x + 8);
+      store8(out + r * D + A, x);
+      store8(out + r * D + B, x + 8);
     }
     return;
   }
@@ -251,7 +253,7 @@ __device__ __forceinline__ void append_block(const T *src, int64_t stride, int n
     Raw16<T> raw[kHold];
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
-      if (r0 + i * RPW + sub < n) raw[i].load(src + (r0 + i * RPW + sub) * stride, A, B);
+      if (r0 + i * RPW + sub < n) raw[i].load(src + static_cast<int64_t>(r0 + i * RPW + sub) * stride, A, B);
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
       if (r0 + i * RPW + sub < n) turned(raw[i], r0 + i * RPW + sub, x[i]);
@@ -269,21 +271,23 @@ __device__ __forceinline__ void append_block(const T *src, int64_t stride, int n
   const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // (a NaN has the largest bits)
   float s = block_scale<F>(amax);
   if (!(s > old) && s == s) s = old;  // the larger; NaN from either stays
-  uint8_t *out = static_cast<uint8_t *>(pages) + dst * D;
+  uint8_t *out = static_cast<uint8_t *>(pages) + static_cast<size_t>(dst) * D;
   if (s > old && held > 0) {  // the rows already there, at the new scale
     const float ratio = old / s;
-    uint8_t *first = out - static_cast<size_t>(held) * D;
+    uint8_t *first = out - held * D;
     for (int r = sub; r < held; r += RPW) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint2 *p = reinterpret_cast<uint2 *>(first + static_cast<size_t>(r) * D + (h ? B : A));
+        uint2 *p = reinterpret_cast<uint2 *>(first + r * D + (h ? B : A));
         float y[8];
         decode8<F>(__ldcg(p), y);
         *p = encode8<F>(y, ratio);
       }
     }
   }
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;  // 0 for a scale of 0 or NaN: codes 0
+  // 0 for a scale of 0 or NaN: codes 0; a power of two is turned over in its exponent
+  float inv = 0.f;
+  if (s > 0.f) inv = F == kFmtI8 ? __frcp_rn(s) : __uint_as_float((254u << 23) - __float_as_uint(s));
 #pragma unroll 1
   for (int r0 = 0; r0 < n; r0 += kHold * RPW) {
     if (n > kHold * RPW) fetch(r0);  // not held: read again
@@ -296,8 +300,8 @@ __device__ __forceinline__ void append_block(const T *src, int64_t stride, int n
           c = encode8<F>(x[i], inv);
           d = encode8<F>(x[i] + 8, inv);
         }
-        *reinterpret_cast<uint2 *>(out + static_cast<size_t>(r) * D + A) = c;
-        *reinterpret_cast<uint2 *>(out + static_cast<size_t>(r) * D + B) = d;
+        *reinterpret_cast<uint2 *>(out + r * D + A) = c;
+        *reinterpret_cast<uint2 *>(out + r * D + B) = d;
       }
     }
   }
@@ -308,7 +312,7 @@ __device__ __forceinline__ void append_block(const T *src, int64_t stride, int n
 // kQPass passes of RPW heads of one row's queries, from head h0 on.
 constexpr int kQPass = 2;
 template <int D, typename T, bool INTER>
-__device__ __forceinline__ void append_queries(const T *q, T *out, int h0, int hq, int rot, const float2 *cs) {
+__device__ __forceinline__ void append_queries(const T *q, T *out, int r, int h0, int hq, int rot, const float2 *cs) {
   constexpr int L = D / 16, RPW = 32 / L;
   const int lane = threadIdx.x & 31, h = h0 + lane / L, unit = lane % L;
   int A, B;
@@ -318,7 +322,7 @@ __device__ __forceinline__ void append_queries(const T *q, T *out, int h0, int h
   for (int i = 0; i < kQPass; ++i)
     if (h + i * RPW < hq) raw[i].load(q + (h + i * RPW) * D, A, B);
   Turn8 t;
-  t.load(cs, unit, rot);
+  t.load(cs, r, unit, rot);
 #pragma unroll
   for (int i = 0; i < kQPass; ++i)
     if (h + i * RPW < hq) {
@@ -333,10 +337,10 @@ __device__ __forceinline__ void append_queries(const T *q, T *out, int h0, int h
 // Grid (x, y): CTA x takes blocks x, x + gridDim.x, .. of the line of all
 // sequences' touched blocks; the y CTAs share a block's heads.
 template <int D, typename T, int FMT, bool INTER>
-__global__ void __launch_bounds__(kApThreads, 3) k_paged_append(const AppendArgs a) {
+__global__ void __launch_bounds__(kApThreads, 5) k_paged_append(const AppendArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  float2 *cs = reinterpret_cast<float2 *>(smem);  // [chunk][rot / 2]
-  uint32_t *pre = reinterpret_cast<uint32_t *>(cs + a.chunk.d * (a.rot / 2));
+  float2 *cs = reinterpret_cast<float2 *>(smem);  // [8 + chunk * rot / 2]
+  uint32_t *pre = reinterpret_cast<uint32_t *>(cs + 8 + a.chunk.d * (a.rot / 2));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk = a.chunk.d, half = a.rot >> 1;
   pdl_wait();
@@ -368,6 +372,7 @@ __global__ void __launch_bounds__(kApThreads, 3) k_paged_append(const AppendArgs
     if (lane == 0) out = x;
   };
   if (warp == 0) prepare(blockIdx.x, units[0]);
+  if (warp == 1 && lane < 8) cs[lane] = make_float2(1.f, 0.f);
   __syncthreads();
   int flip = 0;
   for (uint32_t u = blockIdx.x; u < total; u += gridDim.x, flip ^= 1) {
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(kApThreads, 3) k_paged_append(const AppendArgs
       const float lo = static_cast<float>(fr - static_cast<double>(hi)) * 3.14159265f;
       float sn, cn;
       sincospif(hi, &sn, &cn);
-      cs[i] = make_float2(fmaf(-lo, sn, cn), fmaf(lo, cn, sn));
+      cs[8 + i] = make_float2(fmaf(-lo, sn, cn), fmaf(lo, cn, sn));
     }
     __syncthreads();
     if (warp == 0) prepare(u + gridDim.x, units[flip ^ 1]);
@@ -399,19 +404,19 @@ __global__ void __launch_bounds__(kApThreads, 3) k_paged_append(const AppendArgs
       if (i < kv_tasks) {
         const bool is_v = i >= a.hkv;
         const int h = is_v ? i - a.hkv : i;
-        const size_t ph = static_cast<size_t>(pid) * a.hkv + h;
-        const size_t dst = ph * a.page.d + off, si = ph * a.blocks + a.chunk.div(off);
+        const uint32_t ph = static_cast<uint32_t>(pid) * a.hkv + h, dst = ph * a.page.d + off;  // rows: 32 bits
+        const uint32_t si = ph * a.blocks + a.chunk.div(off);
         if (is_v)
-          append_block<D, T, FMT, INTER, false>(static_cast<const T *>(a.v) + tok * a.v_stride + static_cast<size_t>(h) * D,
-                                         a.v_stride, rows, held, a.vp, dst, a.vs + si, 0, nullptr);
+          append_block<D, T, FMT, INTER, false>(static_cast<const T *>(a.v) + tok * a.v_stride + h * D, a.v_stride, rows,
+                                                held, a.vp, dst, a.vs + si, 0, nullptr);
         else
-          append_block<D, T, FMT, INTER, true>(static_cast<const T *>(a.k) + tok * a.k_stride + static_cast<size_t>(h) * D,
-                                        a.k_stride, rows, held, a.kp, dst, a.ks + si, a.rot, cs);
+          append_block<D, T, FMT, INTER, true>(static_cast<const T *>(a.k) + tok * a.k_stride + h * D, a.k_stride, rows,
+                                               held, a.kp, dst, a.ks + si, a.rot, cs);
       } else {
         const int r = (i - kv_tasks) / groups, grp = (i - kv_tasks) - r * groups;
         append_queries<D, T, INTER>(static_cast<const T *>(a.q) + (tok + r) * a.q_stride,
-                             static_cast<T *>(a.q_out) + (tok + r) * static_cast<int64_t>(a.hq) * D, grp * kHeads, a.hq,
-                             a.rot, cs + r * half);
+                                    static_cast<T *>(a.q_out) + (tok + r) * static_cast<int64_t>(a.hq) * D, r,
+                                    grp * kHeads, a.hq, a.rot, cs);
       }
     }
     __syncthreads();  // the table of sines is read, the next unit is there

@@ -154,7 +154,7 @@ gsa_status launch_append(const AppendArgs &aa, void *stream) {
   // an upper bound of the touched blocks: a sequence's first and last one may be part-filled
   const int chunk = static_cast<int>(aa.chunk.d);
   const int64_t most = std::min<int64_t>(aa.n_tok, aa.n_tok / chunk + 2 * static_cast<int64_t>(aa.B));
-  const size_t smem = static_cast<size_t>(chunk) * (aa.rot / 2) * 8 + (static_cast<size_t>(aa.B) + 1) * 4;
+  const size_t smem = (8 + static_cast<size_t>(chunk) * (aa.rot / 2)) * 8 + (static_cast<size_t>(aa.B) + 1) * 4;
   const auto kern = k_paged_append<D, T, FMT, INTER>;
   static SlotCache cache;
   const int slots = cache.get(kern, kApThreads, smem);
@@ -189,6 +189,7 @@ gsa_status gsa_paged_append(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
   const int64_t qs = adesc->q_stride ? adesc->q_stride : q_row;
   const int64_t ks = adesc->k_stride ? adesc->k_stride : kv_row;
   const int64_t vs = adesc->v_stride ? adesc->v_stride : kv_row;
+  if (q_row > INT32_MAX) return GSA_ERR_UNSUPPORTED;
   if (qs < q_row || ks < kv_row || vs < kv_row || qs % unit || ks % unit || vs % unit) return GSA_ERR_INVALID_ARG;
   for (const void *x : {static_cast<const void *>(page_table), static_cast<const void *>(own_len),
                         static_cast<const void *>(k_pages), static_cast<const void *>(v_pages),
@@ -228,9 +229,9 @@ gsa_status gsa_paged_append(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
   aa.ks = k_scale;
   aa.vs = v_scale;
   aa.q_out = q_out;
-  aa.q_stride = qs;
-  aa.k_stride = ks;
-  aa.v_stride = vs;
+  aa.q_stride = static_cast<int32_t>(qs);
+  aa.k_stride = static_cast<int32_t>(ks);
+  aa.v_stride = static_cast<int32_t>(vs);
   aa.n_tok = adesc->n_tok;
   aa.B = desc->batch;
   aa.hq = desc->hq;
