@@ -464,7 +464,7 @@ gsa_status gsa_prefill(const gsa_desc *desc, const void *q_raw, const void *k_ra
  *   (GSA_DEVERR_BAD_INDEX).  Sequences may share pages that are only read.
  * Rows of sequence b: n_gists[b] * chunk + own_len[b], or own_len[b] where
  * n_gists may be NULL and is (a cache without gists: any length), clamped to
- * t_max.  Gists stay in their own unpaged arrays.  batch <= 8192.  One
+ * t_max.  Gists stay in their own unpaged arrays.  batch <= 8192, hq <= 65535.  One
  * workspace of gsa_workspace_bytes(desc, GSA_OP_PAGED, NULL) bytes serves all
  * of these calls and the score / select calls between them. */
 

@@ -210,9 +210,7 @@ inline int one_wave_splits(int units, int slots, int max_splits) {
 // Launch with programmatic stream serialization: the kernel may start while
 // its predecessor drains; it calls griddepcontrol.wait before touching data.
 template <typename Kern, typename... Args>
-gsa_status launch(Kern kern, dim3 grid, dim3 block, size_t smem, void *stream, const Args &...args) {
-  if (grid.x == 0 || grid.y == 0 || grid.z == 0) return GSA_OK;
-  if (!prepare(kern, smem)) return GSA_ERR_CUDA;
+gsa_status launch_prepared(Kern kern, dim3 grid, dim3 block, size_t smem, void *stream, const Args &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -229,6 +227,13 @@ gsa_status launch(Kern kern, dim3 grid, dim3 block, size_t smem, void *stream, c
     return GSA_ERR_CUDA;
   }
   return GSA_OK;
+}
+
+template <typename Kern, typename... Args>
+gsa_status launch(Kern kern, dim3 grid, dim3 block, size_t smem, void *stream, const Args &...args) {
+  if (grid.x == 0 || grid.y == 0 || grid.z == 0) return GSA_OK;
+  if (!prepare(kern, smem)) return GSA_ERR_CUDA;
+  return launch_prepared(kern, grid, block, smem, stream, args...);
 }
 
 #define GSA_TRY(x)                     \

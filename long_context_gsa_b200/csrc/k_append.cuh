@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kApThreads, 5) k_paged_append(const AppendArgs
         const uint32_t ph = static_cast<uint32_t>(pid) * a.hkv + h, dst = ph * a.page.d + off;  // rows: 32 bits
         const uint32_t si = ph * a.blocks + a.chunk.div(off);
         if (is_v)
-          append_block<D, T, FMT, INTER, false>(static_cast<const T *>(a.v) + tok * a.v_stride + h * D, a.v_stride, rows,
-                                                held, a.vp, dst, a.vs + si, 0, nullptr);
+          append_block<D, T, FMT, INTER, false>(static_cast<const T *>(a.v) + tok * a.v_stride + h * D, a.v_stride,
+                                                rows, held, a.vp, dst, a.vs + si, 0, nullptr);
         else
           append_block<D, T, FMT, INTER, true>(static_cast<const T *>(a.k) + tok * a.k_stride + h * D, a.k_stride, rows,
                                                held, a.kp, dst, a.ks + si, a.rot, cs);

@@ -14,7 +14,7 @@ gsa_status check_paged(const gsa_desc *d, const gsa_pdesc *p) {
   if (p->cache_dtype < GSA_F32 || p->cache_dtype > GSA_E4M3) return GSA_ERR_INVALID_ARG;
   if (p->page < 1 || p->page % d->chunk || p->n_pages < 1 || p->max_pages < 1) return GSA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(p->max_pages) * p->page < d->t_max) return GSA_ERR_INVALID_ARG;
-  if (p->page > (1 << 28) || d->batch > kPgMaxBatch) return GSA_ERR_UNSUPPORTED;
+  if (p->page > (1 << 28) || d->batch > kPgMaxBatch || d->hq > 65535) return GSA_ERR_UNSUPPORTED;
   // rows of the pool are counted in 32 bits
   if (static_cast<int64_t>(p->n_pages) * p->page >= (int64_t(1) << 32) / d->hkv) return GSA_ERR_UNSUPPORTED;
   return GSA_OK;
@@ -66,9 +66,11 @@ gsa_status paged_variant(const gsa_desc *d, const gsa_pdesc *p, Fn fn) {
   return p->cache_dtype == GSA_I8 ? with(D128(), I8()) : with(D128(), E4());
 }
 
-// resident_ctas of one kernel, remembered for each device and amount of shared
-// memory asked for last (the queries cost microseconds, as much as a small
-// call's kernel).
+// CTAs of one kernel that fit on the whole GPU, remembered for each device and
+// the amount of shared memory asked for last (the queries cost microseconds, as
+// much as a small call's kernel); 0 on an error.  The kernel is allowed all the
+// shared memory there is, once: launches from several threads with different
+// amounts must not lower one another's limit.
 struct SlotCache {
   static constexpr int kDevices = 16;
   std::atomic<uint64_t> known[kDevices] = {};  // smem << 32 | CTAs
@@ -80,7 +82,17 @@ struct SlotCache {
       const uint64_t v = known[dev].load(std::memory_order_relaxed);
       if (v && (v >> 32) == smem) return static_cast<int>(v & 0xffffffffu);
     }
-    const int n = resident_ctas(kern, threads, smem);
+    cudaFuncAttributes fa;
+    int optin = 0, per_sm = 0;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             optin - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    const int n = per_sm * sm_count();
     if (keep) known[dev].store(static_cast<uint64_t>(smem) << 32 | static_cast<uint32_t>(n), std::memory_order_relaxed);
     return n;
   }
@@ -92,7 +104,8 @@ gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
   const auto kern = k_paged_attend<D, FMT, QF32, HILO, NT>;
   static SlotCache cache;
   const int grid = std::min(kPgMaxCtas, cache.get(kern, kPgThreads, smem));
-  GSA_TRY(launch(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa));
+  if (grid < 1) return GSA_ERR_CUDA;
+  GSA_TRY(launch_prepared(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa));
   // no segment can have been cut when the longest is short
   if (pa.t_max <= static_cast<int>(kPgWhole) * kPgStep) return GSA_OK;
   return launch(k_paged_join<D, NT>, dim3(grid, PgJoin<D, NT>::kGridY), dim3(256), static_cast<size_t>(grid) * 8 * 4,
@@ -142,10 +155,11 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
     const int k1 = std::max(1, ua.k);
     static SlotCache cache;
     const int slots = cache.get(kern, kUnfoldThreads, paged_unfold_smem<D, F, Q>(k1));
+    if (slots < 1) return GSA_ERR_CUDA;
     const int most = std::max(1, static_cast<int>(static_cast<int64_t>(k1) * d->chunk / (32 * kPuWarps)));
     ua.n_split = one_wave_splits(d->batch * d->hq, slots, std::min(std::min(kUnfoldSplitMax, k1), most));
-    return launch(kern, dim3(ua.n_split, d->hq, d->batch), dim3(kUnfoldThreads),
-                  paged_unfold_smem<D, F, Q>(cdiv(k1, ua.n_split)), stream, pa);
+    return launch_prepared(kern, dim3(ua.n_split, d->hq, d->batch), dim3(kUnfoldThreads),
+                           paged_unfold_smem<D, F, Q>(cdiv(k1, ua.n_split)), stream, pa);
   });
 }
 
@@ -158,12 +172,13 @@ gsa_status launch_append(const AppendArgs &aa, void *stream) {
   const auto kern = k_paged_append<D, T, FMT, INTER>;
   static SlotCache cache;
   const int slots = cache.get(kern, kApThreads, smem);
+  if (slots < 1) return GSA_ERR_CUDA;
   const int x = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, slots)));
   // few blocks: several CTAs share the heads of each, one task a warp
   const int rows = static_cast<int>((aa.n_tok + most - 1) / most);
   const int tasks = 2 * aa.hkv + (aa.q ? rows * cdiv(aa.hq, kQPass * 32 / (D / 16)) : 0);
   const int y = clampi(slots / x, 1, cdiv(tasks, kApWarps));
-  return launch(kern, dim3(x, y), dim3(kApThreads), smem, stream, aa);
+  return launch_prepared(kern, dim3(x, y), dim3(kApThreads), smem, stream, aa);
 }
 
 }  // namespace
@@ -189,7 +204,6 @@ gsa_status gsa_paged_append(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
   const int64_t qs = adesc->q_stride ? adesc->q_stride : q_row;
   const int64_t ks = adesc->k_stride ? adesc->k_stride : kv_row;
   const int64_t vs = adesc->v_stride ? adesc->v_stride : kv_row;
-  if (q_row > INT32_MAX) return GSA_ERR_UNSUPPORTED;
   if (qs < q_row || ks < kv_row || vs < kv_row || qs % unit || ks % unit || vs % unit) return GSA_ERR_INVALID_ARG;
   for (const void *x : {static_cast<const void *>(page_table), static_cast<const void *>(own_len),
                         static_cast<const void *>(k_pages), static_cast<const void *>(v_pages),

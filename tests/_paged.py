@@ -90,7 +90,7 @@ def logit_error(d, reach, floor):
     """How far a base-2 logit may be off.
 
     reach: the largest log2(e) * scale * sum_i |q_i k_i| of an attended row; floor: the same with every |q_i| replaced
-    by the row's largest.  The products of the operands' digits are exact; their fp32 sum over d / 32 matrix instructions a
+    by the row's largest.  The products of the operands' digits are exact; their fp32 sum over d / 32 matrix products a
     digit (at most 6) may truncate at 2^-22 of the largest partial sum each time, which reach bounds within the digits'
     own overlap of 2^-3; the query's digits end at 2^-21 of the row's largest element."""
     return (d / 8 + 5) * 2.0 ** -22 * reach + 2.0 ** -21 * floor

@@ -199,6 +199,40 @@ def test_attend_on_another_stream_and_replayed():
         check_attend(c, 8, 1, q, o2, l2)
 
 
+def test_calls_from_two_threads():
+    """Two host threads with their own streams and workspaces, batches of different sizes (different amounts of shared
+    memory of the same kernel): every call succeeds and gives the bits of the same call alone."""
+    import threading
+    jobs = []
+    for lens, seed in (([130, 7], 21), ([(13 * i) % 40 for i in range(2500)], 22)):
+        c = Cache(lens, 1, 64, 8, 40, "e4m3", seed=seed)
+        q, o, lse, ws, (desc, pdesc, own) = run_attend(c, 2, 1, seed=seed)
+        jobs.append((c, q, o, lse, ws, desc, pdesc, own))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(job):
+        c, q, o, lse, ws, desc, pdesc, own = job
+        stream = torch.cuda.Stream()
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(200):
+                    o2, l2 = torch.zeros_like(o), torch.zeros_like(lse)
+                    G.gsa_paged_attend(desc, pdesc, 1, q, *c.args(), None, own, o2, l2, ws)
+                stream.synchronize()
+            if not (torch.equal(o, o2) and torch.equal(lse, l2)):
+                bad.append("other bits")
+        except Exception as e:  # reported by the test's own thread
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
 # ------------------------------------------------------------------ unfold
 def run_unfold(c, hq, topk, *, dtype="bf16", out="f32", exclude=True, seed=2, sel=None, n_gists=None, prior=None):
     """n_gists: completed chunks of each sequence (the rest of its rows are the own chunk's)."""

@@ -109,6 +109,7 @@ def test_append_pointers(lib):
     assert _append(lib, d, p, _adesc(n_tok=3), cu=None) == 1  # 3 tokens over 2 sequences
     assert _append(lib, d, p, a, nbytes=4096) == 3
     assert _append(lib, _desc(batch=9000), _pdesc(), a) == 2
+    assert _append(lib, _desc(hq=1 << 16, hkv=1 << 13), _pdesc(), a) == 2
     assert _append(lib, d, p, _adesc(n_tok=0), k=None, v=None, q=None, qo=None) == 0  # nothing to do
     assert lib.gsa_paged_append(C.byref(d), None, C.byref(a), *[A] * 15, BIG, None) == 1
     assert lib.gsa_paged_append(C.byref(d), C.byref(p), None, *[A] * 15, BIG, None) == 1
