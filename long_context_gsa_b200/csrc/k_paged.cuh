@@ -73,6 +73,9 @@ constexpr float kPgPScale = 2048.f;  // p is scaled by 2^11 into fp16's range (<
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -313,6 +316,20 @@ struct PgWarp {
     const uint32_t base = ring + st * Cfg::kStage;
     const uint32_t mask = __ballot_sync(0xffffffffu, prow != kNoRow);
     if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + Cfg::kMask), "r"(mask) : "memory");
+    // 32 rows one behind the other (a tile inside a page, or inside a chunk): one address and fixed steps
+    const uint32_t row0 = __shfl_sync(0xffffffffu, prow, 0);
+    if (__all_sync(0xffffffffu, prow == row0 + lane && prow != kNoRow)) {
+      const size_t o8 = static_cast<size_t>(row0 + g) * D + t * 16;
+      const uint8_t *k = kv.k + o8, *v = kv.v + o8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          cp_async16(base + ((i * (D / 64) + c) * 32 + lane) * 16, k + 8 * i * D + 64 * c);
+          cp_async16(base + Cfg::kK + v_off<D>(g + 8 * i, t + 4 * c), v + 8 * i * D + 64 * c);
+        }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // keys g + 8 i
       const uint32_t r = __shfl_sync(0xffffffffu, prow, g + 8 * i);
