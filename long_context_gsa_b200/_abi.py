@@ -495,11 +495,14 @@ def _arg(t, dtype, name, numel, dev, optional=False):
 
 def _rows(t, dtype, name, n_tok, heads, d, stride, dev):
     """Data pointer of token rows [n_tok, heads, d], `stride` elements apart (0: packed)."""
-    want = (stride or heads * d, d, 1)
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dim() != 3 or t.shape[0] < n_tok or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [>= {n_tok}, {heads}, {d}], got {tuple(t.shape)}")
+    want, shape = (stride or heads * d, d, 1), t.shape
+    fits = len(shape) == 3 and shape[0] >= n_tok and shape[1] == heads and shape[2] == d
+    if fits and t.get_device() == dev and t.dtype is dtype and t.stride() == want:
+        return t.data_ptr()
+    if not fits:
+        raise ValueError(f"{name} must be [>= {n_tok}, {heads}, {d}], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the GSA path has no CPU implementation)")
     if t.dtype is not dtype:
@@ -526,8 +529,10 @@ def _cache(desc, pdesc, k_pages, v_pages, k_scale, v_scale, page_table, dev):
 
 def _tail(ws, stream, dev):
     """Workspace pointer and bytes, stream."""
-    p, n = _ws(ws)
-    if ws.get_device() != dev:
+    if isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous():
+        p, n = ws.data_ptr(), ws.numel() * ws.element_size()
+    else:
+        p, n = _ws(ws)
         raise ValueError(f"ws is on {ws.device}, the current device is cuda:{dev}")
     return p, n, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
 
