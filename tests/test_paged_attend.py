@@ -99,6 +99,8 @@ ATTEND = [
     ("e4m3", 128, 16, 2, 32, 64, [5, 200, 129], 3, "bf16", "f32"),   # 24 rows: causal, two groups
     ("i8", 64, 12, 4, 8, 32, [2, 16, 260], 5, "f32", "f32"),     # more queries than rows
     ("e4m3", 64, 16, 1, 16, 64, [64, 300], 64, "bf16", "bf16"),  # the most query tokens
+    ("i8", 128, 4, 1, 16, 48, [3001, 90], 5, "f32", "f32"),      # causal, cut over several CTAs, 16 + 4 rows
+    ("e4m3", 64, 6, 2, 8, 64, [2500], 3, "bf16", "bf16"),
 ]
 
 
@@ -197,6 +199,36 @@ def test_attend_on_another_stream_and_replayed():
         torch.cuda.synchronize()
         c.lens = n
         check_attend(c, 8, 1, q, o2, l2)
+
+
+def test_pool_beyond_4_gb():
+    """Pages whose bytes lie past 2^32 (and whose rows times 128 do): attention, unfolding and an append there."""
+    small = Cache([700], 8, 128, 16, 64, "i8", seed=30)
+    total = (5 << 30) // (8 * 64 * 128)
+    first = total - small.n_pages
+    big = Cache.__new__(Cache)
+    big.__dict__.update(small.__dict__)
+    big.n_pages, big.table = total, (small.table + first).contiguous()
+    big.pages, big.scales = {}, {}
+    for kv in "kv":
+        big.pages[kv] = torch.zeros((total, 8, 64, 128), dtype=torch.int8, device="cuda")
+        big.scales[kv] = torch.zeros((total, 8, 4), device="cuda")
+        big.pages[kv][first:] = small.pages[kv]
+        big.scales[kv][first:] = small.scales[kv]
+    q, o, lse, ws, (desc, _, own) = run_attend(big, 8, 1)
+    check_attend(big, 8, 1, q, o, lse)
+    x, o, lse, _ = run_unfold(big, 8, 9)
+    check_unfold(big, 8, 9, x, o, lse)
+    k = torch.randn((16, 8, 128), device="cuda").to(torch.bfloat16)
+    at = torch.full((1,), 640, dtype=torch.int32, device="cuda")  # block 40
+    pdesc = G.make_pdesc(G.GSA_I8, 64, total, big.max_pages)
+    G.gsa_paged_append(desc, pdesc, G.make_append_desc(16), None, k, k, None, None, None, big.table, None, at,
+                       *big.args()[:4], None, ws)
+    for kv in "kv":
+        got, s = big.rows(kv, 0, 656)[:, 640:], big.scales[kv][int(big.table[0, 10]), :, 0].double()[:, None, None]
+        assert bool(((got - k.transpose(0, 1).double()).abs() <= 0.5 * s * (1 + 2.0 ** -10)).all())
+        assert int(big.pages[kv][:first].count_nonzero()) == 0
+    assert G.gsa_workspace_status(ws) == 0
 
 
 def test_calls_from_two_threads():
@@ -313,6 +345,47 @@ def test_unfold(case):
     x, o, lse, ws = run_unfold(c, hq, topk, dtype=dtype, out=out, exclude=exclude)
     check_unfold(c, hq, topk, x, o, lse, out=out, exclude=exclude)
     assert G.gsa_workspace_status(ws) == 0
+
+
+DECODE = [
+    # fmt, dtype, d, hq, hkv, chunk, lens, topk, exclude
+    ("e4m3", "bf16", 64, 8, 2, 8, [8 * 60 + 3, 8 * 9], 7, True),
+    ("i8", "f32", 128, 4, 1, 16, [16 * 40 + 5], 6, True),
+    ("i8", "bf16", 128, 7, 1, 16, [16 * 40 + 5, 16 * 3], 0, False),  # no selection: the gists and the own chunk
+    ("e4m3", "bf16", 64, 4, 1, 1, [4200], 9, False),                 # rows too long for the selection in the scoring
+]
+
+
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: "{}_{}_d{}_{}x{}_c{}_k{}_x{:d}".format(*c[:6], *c[7:]))
+def test_decode(case):
+    """Score, select and unfold in one call, with and without the outputs that may be left out."""
+    fmt, dtype, d, hq, hkv, chunk, lens, topk, exclude = case
+    c = Cache(lens, hkv, d, chunk, 2 * chunk, fmt, seed=topk + 40)
+    N = [n // chunk for n in lens]
+    g = torch.Generator(device="cuda").manual_seed(41)
+    desc, pdesc, ws = descs(c, hq, dtype=dtype, topk=topk, n_max=max(N), exclude=exclude)
+    B = len(lens)
+    q, gk, gv = (torch.randn(s, generator=g, device="cuda").to(DT[dtype]) for s in
+                 ((B, hq, d), (B, hkv, max(N), d), (B, hkv, max(N), d)))
+    n = torch.tensor(N, dtype=torch.int32, device="cuda")
+    own = torch.tensor([a - b * chunk for a, b in zip(lens, N)], dtype=torch.int32, device="cuda")
+    o, lse, o2 = (torch.empty(s, device="cuda") for s in ((B, hq, d), (B, hq), (B, hq, d)))
+    sel = torch.full((B, hq, max(topk, 1)), -1, dtype=torch.int32, device="cuda")
+    score = torch.empty((B, hq, max(topk, 1)), device="cuda")
+    G.gsa_paged_decode(desc, pdesc, q, gk, gv, *c.args(), n, own, o, lse, sel if topk else None,
+                       score if topk else None, ws)
+    G.gsa_paged_decode(desc, pdesc, q, gk, gv, *c.args(), n, own, o2, None, None, None, ws)
+    assert torch.equal(o, o2) and G.gsa_workspace_status(ws) == 0
+    # the selection is the top of the scores, up to scores that fp32 cannot tell apart
+    for b in range(B):
+        for h in range(hq):
+            z = gk[b, h // (hq // hkv), :N[b]].double() @ q[b, h].double() / math.sqrt(d)
+            got = [m for m in sel[b, h].tolist() if m >= 0]
+            assert len(got) == min(topk, N[b]) == len(set(got))
+            if got:
+                kth = float(z.topk(len(got)).values.min())
+                assert all(float(z[m]) >= kth - 1e-5 * max(1.0, abs(kth)) for m in got)
+    check_unfold(c, hq, topk, dict(q=q, gist_k=gk, gist_v=gv, n=n, sel=sel, score=score), o, lse, exclude=exclude)
 
 
 def test_unfold_own_chunk_full_and_bad_entries():
