@@ -670,12 +670,18 @@ struct PgWarp {
 // (the lengths are on the device, so the cut is too): ragged batches and
 // single long sequences load every SM alike.  A segment begins with kPgHead
 // empty steps on that line, about what starting one costs a CTA, and one of up
-// to kPgWhole steps is not cut.  A segment inside one CTA is written
+// to kPgWhole steps is not cut (64 ragged sequences of up to 3000 rows: 41 us
+// with 0 head steps, 27 with 2, 30 with 8; 37 of up to 9001 rows with 4 fp32
+// query tokens each: 76, 67, 76).  A segment inside one CTA is written
 // directly; of one that several CTAs share each leaves a partial record, which
 // k_paged_join adds up in CTA order.  (Joining by the last CTA to arrive took
 // 10 us of 108 at 4 x 128K rows: 28 records of a segment, one dependent load
-// of a CTA's 4 warps behind the other.)  CTAs of 4 warps, 3 or 4 on an SM: one joins its warps while the
-// others stream.
+// of a CTA's 4 warps behind the other.)  CTAs of 4 warps, 3 or 4 on an SM: one
+// joins its warps while the others stream.
+// Bound by the cache's bytes: 16 x 32K rows of e4m3 take 97 us (5.6 TB/s) and
+// 4 x 128K of int8 107 us (5.0 TB/s, the join of 28 records a segment in it).
+// 16 fp32 query rows are bound by matrix and issue slots: the 37 sequences
+// above, 67 us for 18 us of bytes.
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgStep = 32 * kPgWarps;  // rows of one CTA step
@@ -1011,7 +1017,10 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedAttendArgs a) {
 // the share, in list order, form the 32-row tiles of the warps (a tile may
 // span chunks and pages); one of the 8 query columns is in use.  The gists
 // of selected chunks (exclude mode) are summed on the CUDA cores while the
-// first copies are in flight, as a record of their own.
+// first copies are in flight, as a record of their own.  A CTA streams too
+// little to hide its start and end: top-64 of 16 x 32K rows takes 14.1 us for
+// 5.9 us of bytes, top-128 of 4 x 128K 23.9 for 9.6, 2 x 512K 15.6 for 5.3
+// (neighbouring chunks in place of random ones: the same time).
 struct PagedUnfoldArgs {
   UnfoldArgs u;  // raw_k, raw_v and the tensor maps unused
   PagedKV kv;

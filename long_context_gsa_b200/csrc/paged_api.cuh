@@ -311,6 +311,8 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   pa.chunk = desc->chunk;
   pa.n_max = desc->n_max;
   pa.t_max = desc->t_max;
+  // A CTA takes two steps at least: one sequence of 2000 rows takes 8.1 us with
+  // 1, 8.5 with 2 and 9.7 with 4; 32 of up to 700 rows 16.7, 15.1 and 16.4.
   pa.min_steps = 2;
   pa.scale_log2 = resolve_scale(desc) * kLog2e;
   pa.part = reinterpret_cast<float *>(at(ws, L.pg_part));
