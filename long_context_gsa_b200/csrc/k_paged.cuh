@@ -25,11 +25,11 @@
 //     queries as one fp16 term after a power-of-two scaling of the row to
 //     [2^14, 2^15) (exact for bf16 down to 2^-38 of the largest), fp32 ones as
 //     two (22 bits).
-//   weights: fp16, relative to a power of two near the keys' scales of V and to
-//     a reference weight; one term for bf16 outputs (2^-12 against the 2^-8 of
-//     the output's rounding), two for fp32 (2^-24, or 2^-25 of the largest weight
-//     among keys whose scales lie within 2^10 of the key's).  Tiles of scales
-//     farther apart are taken in several turns (far_apart).
+//   weights: two fp16 terms, relative to a power of two near the keys' scales of V
+//     and to a reference weight (2^-24, or 2^-25 of the largest weight among keys
+//     whose scales lie within 2^10 of the key's); bf16 outputs too, since what
+//     their values cancel to is rounded, not the terms.  Tiles of scales farther
+//     apart are taken in several turns (far_apart).
 // Statistics, sums of weights and the running output are fp32.
 //
 // What bounds it: HBM reads of the codes.  Every warp copies its tiles with
@@ -264,13 +264,12 @@ struct PgQuery {
 };
 
 // The state of one warp over a run of tiles; NT groups of 8 query columns.
-template <int D, int FMT, bool QF32, bool HILO, int NT>
+template <int D, int FMT, bool QF32, int NT>
 struct PgWarp {
   using Cfg = PgCfg<D>;
   using Query = PgQuery<D, FMT, QF32, NT>;
   static constexpr int S = Cfg::kStages;
   static constexpr int MT = D / 16;           // m-tiles of O^T
-  static constexpr int PN = HILO ? 2 : 1;     // fp16 terms of a weight
 
   float m[NT][2], l[NT][2];  // columns 2t, 2t + 1
   float2 o[NT][MT][2];       // O^T: dims g*D/8 + 2j and + 2j + 1, (column 2t, column 2t + 1)
@@ -510,7 +509,7 @@ struct PgWarp {
     float vg[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) vg[i] = ldsf(scb + 128 + 32 * i) * up;
-    uint32_t pb[PN][NT][2][2];  // [term][group][half]: B fragments, keys 2t, 2t + 1 and 2t + 8, 2t + 9
+    uint32_t pb[2][NT][2][2];  // [term][group][half]: B fragments, keys 2t, 2t + 1 and 2t + 8, 2t + 9
     float2 back[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -538,10 +537,8 @@ struct PgWarp {
         for (int i = 0; i < 2; ++i) {
           const uint32_t hi = pack_h2(w[2 * i], w[2 * i + 1]);
           pb[0][nt][h][i] = movmatrix_trans(hi);
-          if (HILO) {
-            const float2 r = unpack_h2(hi);
-            pb[PN - 1][nt][h][i] = movmatrix_trans(pack_h2(w[2 * i] - r.x, w[2 * i + 1] - r.y));
-          }
+          const float2 r = unpack_h2(hi);
+          pb[1][nt][h][i] = movmatrix_trans(pack_h2(w[2 * i] - r.x, w[2 * i + 1] - r.y));
         }
       }
       const float down = __uint_as_float(ref) * (1.f / (1u << kPgUp));
@@ -588,7 +585,7 @@ struct PgWarp {
               mma_f16<true>(d[nt], a0, a1, a2, a3, pb[0][nt][h][0], pb[0][nt][h][1]);
             else
               mma_f16<false>(d[nt], a0, a1, a2, a3, pb[0][nt][h][0], pb[0][nt][h][1]);
-            if (HILO) mma_f16<false>(d[nt], a0, a1, a2, a3, pb[PN - 1][nt][h][0], pb[PN - 1][nt][h][1]);
+            mma_f16<false>(d[nt], a0, a1, a2, a3, pb[1][nt][h][0], pb[1][nt][h][1]);
           }
         }
 #pragma unroll
@@ -866,9 +863,9 @@ __host__ __device__ constexpr uint32_t paged_attend_smem() {
   return kPgWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, NT>);
 }
 
-template <int D, int FMT, bool QF32, bool HILO, int NT>
+template <int D, int FMT, bool QF32, int NT>
 __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(const PagedAttendArgs a) {
-  using Warp = PgWarp<D, FMT, QF32, HILO, NT>;
+  using Warp = PgWarp<D, FMT, QF32, NT>;
   using Query = typename Warp::Query;
   constexpr int R = 8 * NT, kRec = D + kPartHeader;
   static_assert(PgCfg<D>::kRing >= R * kRec * 4, "the warps' results fit over the rings");
@@ -1190,10 +1187,10 @@ __device__ void paged_unfold_finish(const UnfoldArgs &a, size_t row, int split, 
   if (tid == 0 && a.lse) a.lse[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : neg_inf();
 }
 
-template <int D, int FMT, bool QF32, bool HILO>
+template <int D, int FMT, bool QF32>
 __global__ void __launch_bounds__(kUnfoldThreads, PgCfg<D>::kCtas)
     k_paged_unfold(const __grid_constant__ PagedUnfoldArgs pa) {
-  using Warp = PgWarp<D, FMT, QF32, HILO, 1>;
+  using Warp = PgWarp<D, FMT, QF32, 1>;
   using Query = typename Warp::Query;
   const UnfoldArgs &a = pa.u;
   const PagedKV &kv = pa.kv;

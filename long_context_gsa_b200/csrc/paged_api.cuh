@@ -48,9 +48,7 @@ PagedKV paged_kv(const gsa_desc *d, const gsa_pdesc *p, const void *k, const voi
   return kv;
 }
 
-// fn(D, format, fp32 queries, two-term softmax weights) as compile-time
-// constants: two terms when the output keeps more than bf16's 9 bits, and
-// with fp32 queries.
+// fn(D, format, fp32 queries) as compile-time constants.
 template <typename Fn>
 gsa_status paged_variant(const gsa_desc *d, const gsa_pdesc *p, Fn fn) {
   using I8 = std::integral_constant<int, kFmtI8>;
@@ -58,9 +56,7 @@ gsa_status paged_variant(const gsa_desc *d, const gsa_pdesc *p, Fn fn) {
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
   auto with = [&](auto dim, auto fmt) {
-    if (d->dtype == GSA_F32) return fn(dim, fmt, std::true_type(), std::true_type());
-    if (d->out_dtype == GSA_F32) return fn(dim, fmt, std::false_type(), std::true_type());
-    return fn(dim, fmt, std::false_type(), std::false_type());
+    return d->dtype == GSA_F32 ? fn(dim, fmt, std::true_type()) : fn(dim, fmt, std::false_type());
   };
   if (d->d == 64) return p->cache_dtype == GSA_I8 ? with(D64(), I8()) : with(D64(), E4());
   return p->cache_dtype == GSA_I8 ? with(D128(), I8()) : with(D128(), E4());
@@ -98,10 +94,10 @@ struct SlotCache {
   }
 };
 
-template <int D, int FMT, bool QF32, bool HILO, int NT>
+template <int D, int FMT, bool QF32, int NT>
 gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
   const size_t smem = paged_attend_smem<D, FMT, QF32, NT>() + (2 * static_cast<size_t>(pa.B) + 1) * 4;
-  const auto kern = k_paged_attend<D, FMT, QF32, HILO, NT>;
+  const auto kern = k_paged_attend<D, FMT, QF32, NT>;
   static SlotCache cache;
   const int grid = std::min(kPgMaxCtas, cache.get(kern, kPgThreads, smem));
   if (grid < 1) return GSA_ERR_CUDA;
@@ -146,10 +142,10 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
   ua.out_bf16 = d->out_dtype == GSA_BF16;
   ua.lse = lse;
   pa.kv = paged_kv(d, p, k, v, ks, vs, table);
-  return paged_variant(d, p, [&](auto dim, auto fmt, auto qf32, auto hilo) {
+  return paged_variant(d, p, [&](auto dim, auto fmt, auto qf32) {
     constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
     constexpr bool Q = decltype(qf32)::value;
-    const auto kern = k_paged_unfold<D, F, Q, decltype(hilo)::value>;
+    const auto kern = k_paged_unfold<D, F, Q>;
     // residency with the largest list share (one split), then the share of the chosen split count; a split is
     // not made smaller than one 32-row tile a warp
     const int k1 = std::max(1, ua.k);
@@ -321,11 +317,10 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   pa.out = out;
   pa.out_bf16 = desc->out_dtype == GSA_BF16;
   pa.lse = lse;
-  return paged_variant(desc, pdesc, [&](auto dim, auto fmt, auto qf32, auto hilo) {
+  return paged_variant(desc, pdesc, [&](auto dim, auto fmt, auto qf32) {
     constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
-    constexpr bool Q = decltype(qf32)::value, H = decltype(hilo)::value;
-    if (wide) return launch_paged_attend<D, F, Q, H, 2>(pa, stream);
-    return launch_paged_attend<D, F, Q, H, 1>(pa, stream);
+    constexpr bool Q = decltype(qf32)::value;
+    return wide ? launch_paged_attend<D, F, Q, 2>(pa, stream) : launch_paged_attend<D, F, Q, 1>(pa, stream);
   });
 }
 

@@ -1,4 +1,5 @@
-"""The paged readers at the ends of their range: scales of V far apart inside and across tiles.  Bounds are relative to each output's own sum of |weight x value|,
+"""The paged readers at the ends of their range: scales of V far apart inside and across tiles, weights whose values
+cancel.  Bounds are relative to each output's own sum of |weight x value|,
 dim by dim, so that a large value elsewhere hides nothing."""
 import math
 
@@ -86,7 +87,7 @@ def call(c, hq, q, *, dtype, out):
     return o, lse
 
 
-@pytest.mark.parametrize("fmt,d,out", [("e4m3", 64, "f32"), ("i8", 128, "f32")])
+@pytest.mark.parametrize("fmt,d,out", [("e4m3", 64, "f32"), ("i8", 128, "f32"), ("i8", 64, "bf16"), ("e4m3", 128, "bf16")])
 @pytest.mark.parametrize("apart", [10, 11, 20, 40, 90])
 def test_scales_far_apart_in_a_tile(fmt, d, out, apart):
     """Neighbouring blocks of 8 rows whose values differ by 2^apart; the keys make the small ones weigh as much, e^-30
@@ -181,3 +182,18 @@ def strict_parts(q, k, v, gz, gv, s):
     x = torch.cat([v, gv])
     p = torch.exp(z - torch.logsumexp(z, 0))[:, None]
     return (p * x).sum(0), (2.0 ** -12.5) * (p * x.abs()).sum(0)
+
+
+@pytest.mark.parametrize("fmt,d", [("e4m3", 64), ("i8", 64), ("e4m3", 128), ("i8", 128)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_values_that_cancel(fmt, d, out):
+    """Rows in pairs of opposite values under near-equal weights: the output is small beside its terms, so the weights'
+    rounding shows whatever the output's type."""
+    c = Cache([34, 130, 600], 1, d, 2, 32, fmt, seed=8, std=0.5)
+    codes = c.pages["v"].double()
+    codes[:, :, 1::2] = -codes[:, :, ::2]
+    c.pages["v"] = codes.to(c.pages["v"].dtype)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q = (torch.randn((3, 1, 8, d), generator=g, device="cuda") * 0.5).to(torch.bfloat16)
+    o, lse = call(c, 8, q, dtype="bf16", out=out)
+    check(c, 8, 1, q, o, lse, out)
