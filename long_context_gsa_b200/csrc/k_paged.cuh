@@ -17,9 +17,9 @@
 //                  (movmatrix turns the accumulator layout of S^T into it).
 // Operands: codes are exact in fp16 and in int8, and no query or weight is
 // rounded to fewer bits than the result keeps.
-//   int8 keys: m16n8k32 on the codes as they are; a query is 3 digits of 7 bits
-//     (bf16; 2^-20 of the row's largest element) or 4 (fp32; 2^-27), one product
-//     each; sums are exact integers.
+//   int8 keys: m16n8k32 on the codes as they are; a query is 4 digits of 7 bits,
+//     one product each, off by 2^-28 of the row's largest element at most (bf16:
+//     exact down to 2^-19 of it); sums are exact integers.
 //   e4m3 keys: m16n8k16 on fp16 (on sm_100a the e4m3 form of mma.sync runs as
 //     conversions and two fp16 products, so the codes are converted once here);
 //     queries as one fp16 term after a power-of-two scaling of the row to
@@ -188,11 +188,11 @@ __device__ __forceinline__ uint32_t v_off(uint32_t r, uint32_t p) {
 // [NT][term][k-step][lane], and the factor of each row's logits.  Row n
 // (< 8 NT) is row(n), null when unused.
 //   e4m3: kN fp16 terms, k-steps of 16 dims;
-//   int8: kN digits of a fixed-point number |v| < 2^kBits, k-steps of 32 dims.
+//   int8: kN digits of a fixed-point number |v| <= 2^kTopExp, k-steps of 32 dims.
 template <int D, int FMT, bool QF32, int NT>
 struct PgQuery {
   static constexpr bool kI8 = FMT == kFmtI8;
-  static constexpr int kN = kI8 ? (QF32 ? 4 : 3) : (QF32 ? 2 : 1);
+  static constexpr int kN = kI8 ? 4 : (QF32 ? 2 : 1);
   static constexpr int KS = kI8 ? D / 32 : D / 16;
   static constexpr int kTopExp = kI8 ? 7 * kN - 1 : 15;  // the row's largest is brought into [2^(kTopExp-1), 2^kTopExp)
   uint2 frag[NT][kN][KS][32];
@@ -632,15 +632,14 @@ struct PgWarp {
             }
           }
       }
-      // three digits: (d0 128 + d1) 128 + d2; four: (d0 128 + d1) 2^14 + (d2 128 + d3)
-      constexpr float kTop = Query::kN == 4 ? 16384.f : 128.f;
+      static_assert(Query::kN == 4, "(d0 128 + d1) 2^14 + (d2 128 + d3)");
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            z[h][nt][e] = fmaf(static_cast<float>(acc[0][h][nt][e]), kTop, static_cast<float>(acc[1][h][nt][e]));
+            z[h][nt][e] = fmaf(static_cast<float>(acc[0][h][nt][e]), 16384.f, static_cast<float>(acc[1][h][nt][e]));
     } else {
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {

@@ -1,5 +1,5 @@
 """The paged readers at the ends of their range: scales of V far apart inside and across tiles, weights whose values
-cancel.  Bounds are relative to each output's own sum of |weight x value|,
+cancel, queries with elements of very different sizes.  Bounds are relative to each output's own sum of |weight x value|,
 dim by dim, so that a large value elsewhere hides nothing."""
 import math
 
@@ -197,3 +197,19 @@ def test_values_that_cancel(fmt, d, out):
     q = (torch.randn((3, 1, 8, d), generator=g, device="cuda") * 0.5).to(torch.bfloat16)
     o, lse = call(c, 8, q, dtype="bf16", out=out)
     check(c, 8, 1, q, o, lse, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_query_with_one_large_element(fmt, dtype):
+    """An element 2^8 times the others where the keys are 0: the others still count to their last bits."""
+    c = Cache([40, 333], 1, 64, 8, 32, fmt, seed=10)
+    codes = c.pages["k"].double()
+    codes[..., 5] = 0
+    c.pages["k"] = codes.to(c.pages["k"].dtype)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q = torch.randn((2, 1, 4, 64), generator=g, device="cuda")
+    q[..., 5] = 700.0
+    q = q.to(DT[dtype])
+    o, lse = call(c, 4, q, dtype=dtype, out="f32")
+    check(c, 4, 1, q, o, lse, "f32")
