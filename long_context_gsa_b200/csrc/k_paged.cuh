@@ -448,7 +448,8 @@ struct PgWarp {
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = *reinterpret_cast<const float2 *>(&qs.f[8 * nt + 2 * t]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[h][nt][e] *= kg[e >> 1] * (e & 1 ? f.y : f.x);
+        for (int e = 0; e < 4; ++e)  // (in this order: kg f alone may pass fp32's range)
+          z[h][nt][e] = z[h][nt][e] * (e & 1 ? f.y : f.x) * kg[e >> 1];
       }
     }
     if (masked) {

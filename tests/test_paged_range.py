@@ -213,3 +213,17 @@ def test_query_with_one_large_element(fmt, dtype):
     q = q.to(DT[dtype])
     o, lse = call(c, 4, q, dtype=dtype, out="f32")
     check(c, 4, 1, q, o, lse, "f32")
+
+
+def test_logits_whose_factors_pass_fp32():
+    """Keys of 0 in a block with a scale of 2^120 under queries of 2^40: logits of 0, though the product of the two
+    factors is beyond fp32."""
+    for fmt in ("i8", "e4m3"):
+        c = Cache([24], 1, 64, 8, 8, fmt, seed=12)
+        c.pages["k"] = torch.zeros((c.n_pages, 1, 8, 64), device="cuda").to(c.pages["k"].dtype)
+        c.scales["k"].fill_(2.0 ** 120)
+        q = torch.full((1, 1, 2, 64), 2.0 ** 40, device="cuda", dtype=torch.bfloat16)
+        o, lse = call(c, 2, q, dtype="bf16", out="f32")
+        v = c.rows("v", 0, 24)[0]
+        assert bool(((o[0, 0].double() - v.mean(0)).abs() <= 2.0 ** -19 * v.abs().mean(0)).all())
+        assert bool(((lse - math.log(24)).abs() <= 2.0 ** -19).all())
