@@ -110,12 +110,15 @@ __device__ __forceinline__ void unit_dims(int i, int rot, int &A, int &B) {
   B = halves ? (rot >> 1) + 8 * i : 16 * i + 8;
 }
 
-// The unit's 8 (cos, sin); for dims that are not turned the 8 times (1, 0)
-// that the table begins with (its rows of rot / 2 follow).
+// The unit's 8 (cos, sin).  Dims that are not turned pass through as they are
+// (times (1, 0) an inf would make its partner a NaN, and a -0 lose its sign);
+// they load the 8 that the table begins with (its rows of rot / 2 follow).
 struct Turn8 {
   float4 c[4];
+  bool on;
   __device__ __forceinline__ void load(const float2 *cs, int r, int i, int rot) {
-    const float4 *p = reinterpret_cast<const float4 *>(i < (rot >> 4) ? cs + 8 + r * (rot >> 1) + 8 * i : cs);
+    on = i < (rot >> 4);
+    const float4 *p = reinterpret_cast<const float4 *>(on ? cs + 8 + r * (rot >> 1) + 8 * i : cs);
 #pragma unroll
     for (int k = 0; k < 4; ++k) c[k] = p[k];
   }
@@ -132,9 +135,9 @@ struct Turn8 {
   }
   __device__ __forceinline__ void pair(int k, float &u, float &v) const {
     const float cs = k & 1 ? c[k / 2].z : c[k / 2].x, sn = k & 1 ? c[k / 2].w : c[k / 2].y;
-    const float p = fmaf(u, cs, -(v * sn));
-    v = fmaf(v, cs, u * sn);
-    u = p;
+    const float p = fmaf(u, cs, -(v * sn)), q = fmaf(v, cs, u * sn);
+    u = on ? p : u;
+    v = on ? q : v;
   }
 };
 
