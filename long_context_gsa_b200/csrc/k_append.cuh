@@ -177,9 +177,12 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
-// Eight codes of x * inv.
-template <int FMT>
-__device__ __forceinline__ uint2 encode8(const float *x, float inv) {
+// Eight codes of x inv.  DIV: of x / s, inv the rounded 1 / s.  int8: x inv
+// alone is off by up to 3 half units in the last place, which takes a quotient
+// next to a half step to the wrong side; one correction by the remainder gives
+// the nearest fp32 one.  (e4m3's scales are powers of two.)
+template <int FMT, bool DIV = false>
+__device__ __forceinline__ uint2 encode8(const float *x, float inv, float s = 0.f) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -188,7 +191,9 @@ __device__ __forceinline__ uint2 encode8(const float *x, float inv) {
       uint32_t u = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int c = min(max(__float2int_rn(y[i] * inv), -127), 127);
+        float v = y[i] * inv;
+        if (DIV) v = fmaf(fmaf(-v, s, y[i]), inv, v);
+        const int c = min(max(__float2int_rn(v), -127), 127);
         u |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
       }
       w[h] = u;
@@ -300,8 +305,8 @@ __device__ __forceinline__ void append_block(const T *src, int stride, int n, in
       if (r < n) {
         uint2 c = make_uint2(0, 0), d = make_uint2(0, 0);
         if (inv > 0.f) {
-          c = encode8<F>(x[i], inv);
-          d = encode8<F>(x[i] + 8, inv);
+          c = encode8<F, true>(x[i], inv, s);
+          d = encode8<F, true>(x[i] + 8, inv, s);
         }
         *reinterpret_cast<uint2 *>(out + r * D + A) = c;
         *reinterpret_cast<uint2 *>(out + r * D + B) = d;

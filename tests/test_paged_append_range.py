@@ -1,4 +1,4 @@
-"""gsa_paged_append at the ends of its range: dims that no position turns."""
+"""gsa_paged_append at the ends of its range: dims that no position turns, quotients next to a half step."""
 import math
 
 import pytest
@@ -57,3 +57,32 @@ def test_dims_that_are_not_turned_keep_their_bits(dtype, inter, d, rot):
         for kv, x, first in (("k", k, rot), ("v", v, 0)):
             got = p.pages[kv][pid, :, at % 16, first:]
             assert torch.equal(got.view(word), x[13 * b:13 * b + 13, :, first:].contiguous().view(word)), kv
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_int8_quotients_next_to_half_steps(dtype):
+    """Values within a few fp32 steps of (k + 1/2) scales: a code is off by half a step of the exact quotient, plus the
+    rounding of the quotient to fp32 (half of 2^-17 below 128; a reciprocal's would be up to three times that)."""
+    d, blocks = 128, 64
+    p = Pool(1, 1, d, 64, 64, 64 * blocks, "i8")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    top = torch.exp(3 * torch.randn((blocks, 1, 1), generator=g, device="cuda"))  # each block's largest
+    if dtype == "bf16":
+        top = top.to(torch.bfloat16).float()
+    s = (top.double() / 127).float()
+    half = torch.randint(0, 127, (blocks, 64, d), generator=g, device="cuda") + 0.5
+    x = (half.double() * s.double()).to(DT[dtype])
+    if dtype == "f32":
+        near = torch.randint(-2, 3, x.shape, generator=g, device="cuda", dtype=torch.int32)
+        x = (x.view(torch.int32) + near).view(torch.float32)
+    x = x * (1 - 2 * torch.randint(0, 2, x.shape, generator=g, device="cuda")).to(x.dtype)
+    x[:, :1, :1] = top.to(x.dtype)
+    x = x.clamp(-top.to(x.dtype), top.to(x.dtype)).view(blocks * 64, 1, d).contiguous()
+    plain_append(p, p.desc(1, dtype), torch.zeros((len(x), 1, d), dtype=x.dtype, device="cuda"), x, x, 0, False,
+                 torch.zeros(1, dtype=torch.int32, device="cuda"))
+    for kv in "kv":
+        pid = p.table[0].long()
+        assert torch.equal(p.scales[kv][pid, 0, 0], s.flatten())
+        code = p.pages[kv][pid, 0].double()
+        off = (x.view(blocks, 64, d).double() / s.double() - code).abs()
+        assert float(off.max()) <= 0.5 + 2.0 ** -18 + 2.0 ** -40, float(off.max()) - 0.5
