@@ -152,7 +152,8 @@ Layout layout(const gsa_desc *d, int32_t op, const gsa_hdesc *h) {
     take(L.gs_plus, static_cast<size_t>(d->batch) * 4);
   }
   if (op == GSA_OP_PAGED) {
-    take(L.pg_append, 256);
+    // the counter that must stay zero between calls: at one place whatever the shapes
+    L.pg_append = L.status + 64;
     take(L.pg_joins, static_cast<size_t>(kPgMaxCtas) * sizeof(int4));
     take(L.pg_part, static_cast<size_t>(kPgMaxCtas) * 2 * kPgMaxRows * rec);
     take(L.gs_cur, static_cast<size_t>(d->batch) * 4);  // gsa_paged_gist_step runs in this workspace too
