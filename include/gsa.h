@@ -161,7 +161,11 @@ int32_t gsa_version(void);
 size_t gsa_workspace_bytes(const gsa_desc *desc, int32_t op, const gsa_hdesc *hdesc);
 
 /* Zero the workspace on `stream` (cudaMemsetAsync).  Needed once after
- * allocation; every call leaves the workspace reusable afterwards. */
+ * allocation; every call leaves the workspace reusable afterwards.  The fused
+ * decode steps (gsa_decode, gsa_score_select, gsa_paged_decode) keep counters
+ * in it, behind one another for batch * hq rows: call it again before one of
+ * them when calls of another batch * hq, or prefill or multi-query calls, used
+ * the workspace in between.  The other fields of the descriptors may differ. */
 gsa_status gsa_workspace_init(void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronise `stream`, copy the workspace status word (GSA_DEVERR_* bits)

@@ -1110,6 +1110,14 @@ struct PagedUnfoldArgs {
 
 constexpr int kPuWarps = kUnfoldWarps;
 
+// Zeroes the counters of rows whose splits are about to be joined.
+__global__ void __launch_bounds__(256) k_paged_arm(uint32_t *counters, int rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < rows) counters[i] = 0u;
+}
+
 // rings (over them, once drained, the warps' results) | queries | items (the last one for the own chunk)
 struct PagedItem {
   uint32_t prow;  // pool row of the chunk's first row, kNoRow: page outside the pool

@@ -112,7 +112,7 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
                             const float *ks, const float *vs, const int32_t *table, const void *gist_v,
                             const int32_t *n_gists, const int32_t *own_len, const int32_t *sel_idx,
                             const float *sel_score, const float *prior, int n_prior, void *out, float *lse,
-                            const Layout &L, void *ws, void *stream, uint32_t *ready = nullptr) {
+                            const Layout &L, void *ws, void *stream, bool armed, uint32_t *ready = nullptr) {
   PagedUnfoldArgs pa;
   std::memset(static_cast<void *>(&pa), 0, sizeof(pa));
   UnfoldArgs &ua = pa.u;
@@ -154,6 +154,11 @@ gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q
     if (slots < 1) return GSA_ERR_CUDA;
     const int most = std::max(1, static_cast<int>(static_cast<int64_t>(k1) * d->chunk / (32 * kPuWarps)));
     ua.n_split = one_wave_splits(d->batch * d->hq, slots, std::min(std::min(kUnfoldSplitMax, k1), most));
+    // The rows' counters must be zero.  In the fused step the scoring or the selection has re-armed them; here a
+    // kernel does (0.5 us of 17; a memset, which no kernel starts ahead of, 4).
+    if (ua.n_split > 1 && !armed)
+      GSA_TRY(launch_prepared(k_paged_arm, dim3(cdiv(ua.ready.rows, 256)), dim3(256), 0, stream, ua.counters,
+                              ua.ready.rows));
     return launch_prepared(kern, dim3(ua.n_split, d->hq, d->batch), dim3(kUnfoldThreads),
                            paged_unfold_smem<D, F, Q>(cdiv(k1, ua.n_split)), stream, pa);
   });
@@ -354,7 +359,7 @@ gsa_status gsa_paged_unfold(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
                                        : (prior == GSA_PRIOR_HGSA ? 1 : 2) * hgsa_splits(desc);
   }
   return run_paged_unfold(desc, pdesc, q, k_pages, v_pages, k_scale, v_scale, page_table, gist_v, n_gists, own_len,
-                          sel_idx, sel_score, pr, n_prior, out, lse, L, ws, stream);
+                          sel_idx, sel_score, pr, n_prior, out, lse, L, ws, stream, false);
 }
 
 gsa_status gsa_paged_decode(const gsa_desc *desc, const gsa_pdesc *pdesc, const void *q, const void *gist_k,
@@ -392,7 +397,7 @@ gsa_status gsa_paged_decode(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
                        si, ss, counters, stream));
   }
   return run_paged_unfold(desc, pdesc, q, k_pages, v_pages, k_scale, v_scale, page_table, gist_v, n_gists, own_len, si,
-                          ss, part, part ? n_prior : 0, out, lse, L, ws, stream, ready);
+                          ss, part, part ? n_prior : 0, out, lse, L, ws, stream, desc->topk > 0 || ready, ready);
 }
 
 gsa_status gsa_paged_gist_step(const gsa_desc *desc, const gsa_pdesc *pdesc, const void *q, const void *k_new,
@@ -415,7 +420,7 @@ gsa_status gsa_paged_gist_step(const gsa_desc *desc, const gsa_pdesc *pdesc, con
   const int32_t *n_plus = reinterpret_cast<int32_t *>(at(ws, L.gs_plus));
   GSA_TRY(run_paged_unfold(&g, pdesc, q, k_pages, v_pages, k_scale, v_scale, page_table, gist_v, n_cur, own_len,
                            nullptr, nullptr, reinterpret_cast<float *>(at(ws, L.part_g)), n_prior, out, lse, L, ws,
-                           stream));
+                           stream, false));
   return launch(k_gist_commit, dim3(cdiv(g.batch, 128)), dim3(128), 0, stream, n_cur, n_plus, n_gists, own_len,
                 static_cast<int>(g.batch));
 }
