@@ -1,10 +1,13 @@
-"""One workspace under several descriptors: what a paged call leaves in it, or finds there, does not reach the next."""
+"""Paged calls beside others: one workspace under several descriptors, several threads at once, selections of the
+hierarchical calls."""
+import threading
+
 import pytest
 import torch
 
 from _paged import Cache
 from test_paged_append import Pool, append, check_append
-from test_paged_attend import check_unfold, code_of, descs, run_unfold
+from test_paged_attend import check_unfold, code_of, descs, run_attend, run_unfold
 
 pytestmark = pytest.mark.gpu
 
@@ -70,4 +73,87 @@ def test_unfold_joins_its_rows_whatever_the_workspace_served_before():
                            G.GSA_PRIOR_NONE, o2, lse2, ws)
         assert torch.equal(o2, o) and torch.equal(lse2, lse)
         G.gsa_workspace_init(ws)  # (the fused step of the small batch, after another one's calls)
+    assert G.gsa_workspace_status(ws) == 0
+
+
+def test_every_call_from_two_threads_gives_the_same_bits():
+    """Two host threads begin together, each with its own stream and workspace and other amounts of shared memory; each
+    of their calls is compared on its stream."""
+    jobs = []
+    for lens, seed in (([130, 7], 21), ([(13 * i) % 40 for i in range(2500)], 22)):
+        c = Cache(lens, 1, 64, 8, 40, "e4m3", seed=seed)
+        q, o, lse, ws, (desc, pdesc, own) = run_attend(c, 2, 1, seed=seed)
+        jobs.append((c, q, o, lse, ws, desc, pdesc, own, torch.zeros((), dtype=torch.bool, device="cuda")))
+    torch.cuda.synchronize()
+    start, bad = threading.Barrier(2), []
+
+    def work(c, q, o, lse, ws, desc, pdesc, own, off):
+        stream = torch.cuda.Stream()
+        try:
+            with torch.cuda.stream(stream):
+                o2, l2 = torch.zeros_like(o), torch.zeros_like(lse)
+                start.wait(60)
+                for _ in range(200):
+                    o2.zero_()
+                    l2.zero_()
+                    G.gsa_paged_attend(desc, pdesc, 1, q, *c.args(), None, own, o2, l2, ws)
+                    off |= (o2 != o).any() | (l2 != lse).any()
+                stream.synchronize()
+        except Exception as e:  # reported by the test's own thread
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+    assert not any(bool(j[-1]) for j in jobs)
+
+
+@pytest.mark.parametrize("levels", [1, 2])
+@pytest.mark.parametrize("exclude", [False, True])
+def test_hierarchical_selections_feed_the_paged_unfold(levels, exclude):
+    """hgsa_select / hgsa2_select, then gsa_paged_unfold: the outputs of gsa_unfold_attend on the same selection and
+    partial, over raw rows that hold the codes' values exactly (e4m3 codes, power-of-two scales, bf16)."""
+    B, hq, hkv, d, chunk, N = 2, 8, 2, 64, 8, 64
+    c = Cache([N * chunk + 5, N * chunk + 1], hkv, d, chunk, 32, "e4m3", seed=3)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, gk, gv, mk, mv, m2k, m2v = rnd(B, hq, d), *(rnd(B, hkv, n, d) for n in (N, N, 16, 16, 4, 4))
+    n = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    own = torch.tensor([5, 1], dtype=torch.int32, device="cuda")
+    desc = G.make_desc(B, hq, hkv, d, chunk, N, c.cap, 6, exclude)
+    pdesc = G.make_pdesc(G.GSA_E4M3, c.page, c.n_pages, c.max_pages)
+    raw = {kv: torch.zeros((B, hkv, c.cap, d), dtype=torch.bfloat16, device="cuda") for kv in "kv"}
+    for kv in "kv":
+        for b in range(B):
+            raw[kv][b, :, :c.lens[b]] = c.rows(kv, b, c.lens[b]).to(torch.bfloat16)
+            assert torch.equal(raw[kv][b, :, :c.lens[b]].double(), c.rows(kv, b, c.lens[b]))
+    h1 = G.make_hdesc(4, 3, 16)
+    hd = h1 if levels == 1 else G.make_h2desc(h1, G.make_hdesc(4, 2, 4))
+    ws = torch.empty(G.gsa_workspace_bytes(desc, (G.GSA_OP_HGSA, G.GSA_OP_HGSA2)[levels - 1], hd), dtype=torch.uint8,
+                     device="cuda")
+    G.gsa_workspace_init(ws)
+    idx = lambda k: torch.empty((B, hq, k), dtype=torch.int32, device="cuda")  # noqa: E731
+    si, ss = idx(6), torch.empty((B, hq, 6), device="cuda")
+    outs = []
+    for paged in (True, False):
+        if levels == 1:
+            G.hgsa_select(desc, hd, q, mk, mv, gk, gv, n, idx(3), si, ss, ws)
+        else:
+            G.hgsa2_select(desc, hd, q, m2k, m2v, mk, mv, gk, gv, n, idx(2), idx(3), si, ss, ws)
+        prior = G.GSA_PRIOR_NONE if exclude else (G.GSA_PRIOR_HGSA, G.GSA_PRIOR_HGSA2)[levels - 1]
+        o, lse = torch.empty((B, hq, d), device="cuda"), torch.empty((B, hq), device="cuda")
+        if paged:
+            G.gsa_paged_unfold(desc, pdesc, q, *c.args(), gv, n, own, si, ss, prior, o, lse, ws)
+        else:
+            G.gsa_unfold_attend(desc, q, raw["k"], raw["v"], gv, n, own, si, ss, prior, o, lse, ws)
+        outs.append((o, lse))
+    # The partial and the selection are the same bits.  Both unfolds' logits sum bf16 products in fp32 (reach below
+    # 2^6 here: 2^-15 of a weight), the unpaged one's weights are two bf16 terms (2^-16): 2^-13 of the largest value
+    # covers twice their sum.
+    vmax = max(float(raw["v"].abs().max()), float(gv.abs().max()), float(mv.abs().max()))
+    assert float((outs[0][0] - outs[1][0]).abs().max()) <= 2.0 ** -13 * vmax
+    assert float((outs[0][1] - outs[1][1]).abs().max()) <= 2.0 ** -14
     assert G.gsa_workspace_status(ws) == 0
