@@ -1017,27 +1017,20 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
 }
 
 // Grid (ctas, R / kRows) behind k_paged_attend: CTA (c, y) adds up kRows rows
-// of the cut segment that begins in c's part, kWarps warps a row.  The records
+// of the cut segment that begins in c's part, W warps a row.  The records
 // lie equally spaced (the first one's in slot 1, the others in slot 0); a
 // row's warps share them out (D / 4 lanes a record), the first kBatch of a lane
 // fetched while the weights (a record a lane, by every warp for itself) are
 // made.
-template <int D, int NT>
-struct PgJoin {
-  static constexpr int kWarps = D == 128 ? 4 : 1;  // 28 records of 128 dims at 4 x 128K rows, 6 of 64 at 16 x 32K
-  static constexpr int kRows = 8 / kWarps, kGridY = NT * kWarps;
-};
-
-template <int D, int NT>
+template <int D, int NT, int W>
 __global__ void __launch_bounds__(256) k_paged_join(const PagedAttendArgs a) {
-  using J = PgJoin<D, NT>;
-  constexpr int R = 8 * NT, kRec = D + kPartHeader, kStride = 2 * R * kRec;
-  constexpr int kSub = 128 / D, kBatch = 8, kEach = J::kWarps * kSub;  // records side by side in a row's warps
-  extern __shared__ float cw[];                                        // [8][ctas] weights
+  constexpr int R = 8 * NT, kRec = D + kPartHeader, kStride = 2 * R * kRec, kRows = 8 / W;
+  constexpr int kSub = 128 / D, kBatch = 8, kEach = W * kSub;  // records side by side in a row's warps
+  extern __shared__ float cw[];                                // [8][ctas] weights
   __shared__ float4 sums[8][32];
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % J::kWarps;
-  const int r = J::kRows * blockIdx.y + warp / J::kWarps;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+  const int r = kRows * blockIdx.y + warp / W;
   const int first = part * kSub + lane / (D / 4), d = 4 * (lane % (D / 4));
   const int c0 = blockIdx.x;
   const int4 join = __ldcg(a.joins + c0);

@@ -104,8 +104,14 @@ gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
   GSA_TRY(launch_prepared(kern, dim3(grid), dim3(kPgThreads), smem, stream, pa));
   // no segment can have been cut when the longest is short
   if (pa.t_max <= static_cast<int>(kPgWhole) * kPgStep) return GSA_OK;
-  return launch(k_paged_join<D, NT>, dim3(grid, PgJoin<D, NT>::kGridY), dim3(256), static_cast<size_t>(grid) * 8 * 4,
-                stream, pa);
+  const size_t weights = static_cast<size_t>(grid) * 8 * 4;
+  // Four warps a row where a segment has many records, 12 or more if they are of one length; one where it has few and
+  // the join is short: 1 x 32K rows of d = 64 (74 records) 21.7 and 23.6 us, 1 x 128K of d = 128 (111) 47.4 and 56.9,
+  // 4 x 32K (18) 34.3 and 34.8; 16 x 32K of d = 128 (7) 113.0 and 112.1, of d = 64 (5) 98.9 and 98.1, 32 x 8K of
+  // d = 128 (3) 68.3 and 67.0, 16 x 2K of d = 64 (5) 18.6 and 17.7.
+  if (grid >= 12ll * pa.B * pa.kv.hkv * pa.rg)
+    return launch(k_paged_join<D, NT, 4>, dim3(grid, 4 * NT), dim3(256), weights, stream, pa);
+  return launch(k_paged_join<D, NT, 1>, dim3(grid, NT), dim3(256), weights, stream, pa);
 }
 
 gsa_status run_paged_unfold(const gsa_desc *d, const gsa_pdesc *p, const void *q, const void *k, const void *v,

@@ -227,3 +227,32 @@ def test_logits_whose_factors_pass_fp32():
         v = c.rows("v", 0, 24)[0]
         assert bool(((o[0, 0].double() - v.mean(0)).abs() <= 2.0 ** -19 * v.abs().mean(0)).all())
         assert bool(((lse - math.log(24)).abs() <= 2.0 ** -19).all())
+
+
+@pytest.mark.parametrize("fmt,d,n_q", [("e4m3", 64, 1), ("i8", 128, 1), ("i8", 64, 4), ("e4m3", 128, 4)])
+def test_many_segments_each_cut(fmt, d, n_q):
+    """16 sequences x 4 kv heads, most of them shared by a few CTAs: few records to a segment."""
+    c = Cache([2600 + 37 * i for i in range(14)] + [0, 90], 4, d, 16, 48, fmt, seed=n_q)
+    q, o, lse, ws, _ = run_attend(c, 16, n_q, dtype="bf16")
+    assert not o[14].any() and bool((lse[14] == -math.inf).all())
+    for b in (0, 3, 6, 9, 13, 15):
+        k, v = c.rows("k", b, c.lens[b]), c.rows("v", b, c.lens[b])
+        for i in range(n_q):
+            end = c.lens[b] - (n_q - 1) + i
+            for h in range(0, 16, 3):
+                strict(o[b, i, h], lse[b, i, h], q[b, i, h].double(), k[h // 4, :end], v[h // 4, :end],
+                       1 / math.sqrt(d), f"seq {b} query {i} head {h}")
+    assert G.gsa_workspace_status(ws) == 0
+
+
+def test_nothing_cached_anywhere():
+    """A batch without a single row: zeros and empty sums, in one call and in a batch of the largest size."""
+    for lens in ([0], [0] * 8192):
+        c = Cache.__new__(Cache)
+        c.lens, c.hkv, c.d, c.chunk, c.page, c.fmt, c.cap = lens, 1, 64, 8, 8, "i8", 8
+        c.max_pages, c.n_pages = 1, 1
+        c.table = torch.full((len(lens), 1), -1, dtype=torch.int32, device="cuda")
+        c.pages = {kv: torch.full((1, 1, 8, 64), -128, dtype=torch.int8, device="cuda") for kv in "kv"}
+        c.scales = {kv: torch.full((1, 1, 1), float("nan"), device="cuda") for kv in "kv"}
+        q, o, lse, ws, _ = run_attend(c, 2, 2)
+        assert not o.any() and bool((lse == -math.inf).all()) and G.gsa_workspace_status(ws) == 0
