@@ -105,11 +105,13 @@ gsa_status launch_paged_attend(const PagedAttendArgs &pa, void *stream) {
   // no segment can have been cut when the longest is short
   if (pa.t_max <= static_cast<int>(kPgWhole) * kPgStep) return GSA_OK;
   const size_t weights = static_cast<size_t>(grid) * 8 * 4;
-  // Four warps a row where a segment has many records, 12 or more if they are of one length; one where it has few and
+  // Four warps a row where a segment has many records, 12 or more if all are of length t_max; one where it has few and
   // the join is short: 1 x 32K rows of d = 64 (74 records) 21.7 and 23.6 us, 1 x 128K of d = 128 (111) 47.4 and 56.9,
   // 4 x 32K (18) 34.3 and 34.8; 16 x 32K of d = 128 (7) 113.0 and 112.1, of d = 64 (5) 98.9 and 98.1, 32 x 8K of
   // d = 128 (3) 68.3 and 67.0, 16 x 2K of d = 64 (5) 18.6 and 17.7.
-  if (grid >= 12ll * pa.B * pa.kv.hkv * pa.rg)
+  const int64_t segments = static_cast<int64_t>(pa.B) * pa.kv.hkv * pa.rg;
+  const int longest = (cdiv(pa.t_max, kPgStep) + static_cast<int>(kPgHead)) / pa.min_steps;
+  if (std::min<int64_t>(grid / segments, longest) >= 12)
     return launch(k_paged_join<D, NT, 4>, dim3(grid, 4 * NT), dim3(256), weights, stream, pa);
   return launch(k_paged_join<D, NT, 1>, dim3(grid, NT), dim3(256), weights, stream, pa);
 }
@@ -230,7 +232,7 @@ gsa_status gsa_paged_append(const gsa_desc *desc, const gsa_pdesc *pdesc, const 
   }
   if (q_new) {
     GSA_TRY(need_ptr(q_out));
-    if (q_out == q_new) return GSA_ERR_INVALID_ARG;  // a lane reads its partner's dims
+    if (q_out == q_new) return GSA_ERR_INVALID_ARG;  // queries are read as data that nobody writes meanwhile
   }
   const Layout L = layout(desc, GSA_OP_PAGED, nullptr);
   if (ws_bytes < L.total) return GSA_ERR_WORKSPACE;
@@ -318,8 +320,8 @@ gsa_status gsa_paged_attend(const gsa_desc *desc, const gsa_pdesc *pdesc, int32_
   pa.chunk = desc->chunk;
   pa.n_max = desc->n_max;
   pa.t_max = desc->t_max;
-  // A CTA takes two steps at least: one sequence of 2000 rows takes 8.1 us with
-  // 1, 8.5 with 2 and 9.7 with 4; 32 of up to 700 rows 16.7, 15.1 and 16.4.
+  // A CTA takes two steps at least: one sequence of 2000 rows takes 8.7 us with
+  // 1, 9.2 with 2 and 10.6 with 4; 32 of up to 700 rows 17.5, 16.0 and 17.3.
   pa.min_steps = 2;
   pa.scale_log2 = resolve_scale(desc) * kLog2e;
   pa.part = reinterpret_cast<float *>(at(ws, L.pg_part));
