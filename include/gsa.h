@@ -131,7 +131,8 @@ typedef struct gsa_h2desc {
 /* A paged raw-token cache.  Raw row r of sequence b lies in page
  * page_table[b][r / page] at row r % page of it. */
 typedef struct gsa_pdesc {
-  int32_t cache_dtype; /* GSA_I8 or GSA_E4M3; gsa_paged_append also desc->dtype (no scales) */
+  int32_t cache_dtype; /* GSA_I8 or GSA_E4M3.  gsa_paged_append also takes desc->dtype (no scales), which the
+                        * calls that read pages refuse: with page = t_max such a pool is the unpaged calls' cache */
   int32_t page;        /* rows per page: a multiple of desc->chunk */
   int32_t n_pages;     /* pages of the pool; n_pages * page * hkv < 2^32 */
   int32_t max_pages;   /* page-table entries per sequence; max_pages * page >= t_max */
@@ -462,7 +463,9 @@ gsa_status gsa_prefill(const gsa_desc *desc, const void *q_raw, const void *k_ra
  * rows and kv head: s = max|x| / 127 (GSA_I8) or the least power of two with
  * max|x| / s <= 448 (GSA_E4M3).  Scales are 0 (a block of zeros: max|x| below
  * 2^-100), between 2^-110 and 2^126, or NaN (a block that received an inf or
- * NaN; every row of it reads as NaN).
+ * NaN; every row of it reads as NaN).  Attention is right over that range, and
+ * fastest where the scales of V lie within 2^10 of one another.  Weighted sums
+ * are fp32: they may overflow for values beyond 2^124 / rows.
  *   page_table [batch, max_pages] int32; entries past a sequence's rows are
  *   not read.  A row whose page lies outside the pool is left out and flagged
  *   (GSA_DEVERR_BAD_INDEX).  Sequences may share pages that are only read.

@@ -20,12 +20,14 @@
 // blocks), so the sines of a row are computed once and every block of codes
 // has one writer; a warp takes one (block, head) of keys or values, or one
 // row's queries of a few heads, at a time.  A lane works on a unit of 16 dims,
-// the 8 pairs that turn together, so nothing is loaded twice, and a block of
-// up to kHold passes of rows stays in registers between its maximum and its
-// codes.  32768 tokens, 32 / 8 heads of 64 dims, e4m3 (369 MB): 127 us with 8
-// dims a lane, each lane loading its partner's too and an index division a
-// row; 86 us so (4.3 TB/s).  CTAs of 128 threads, 5 on an SM: 256 threads took
-// 87..94 us, 64 threads as long; more queries in flight a lane spill.
+// the 8 pairs that turn together, so nothing is loaded twice.  A block's first
+// kHold passes of rows (8 rows of 64 dims or 4 of 128) stay in registers between
+// its maximum and its codes, larger blocks are loaded and turned again (their
+// second read from L2).  32768 tokens, 32 / 8 heads of 64 dims, e4m3 (369 MB):
+// 127 us with 8 dims a lane, each lane loading its partner's too and an index
+// division a row; 87 us so (4.2 TB/s).  CTAs of 128 threads, 5 on an SM: 256
+// threads took 87..94 us, 64 threads as long; more queries in flight a lane
+// spill.
 #pragma once
 
 #include <cuda_fp8.h>

@@ -15,16 +15,16 @@
 //                  kPgSlack), the scale of K applied to z, that of V to p;
 //   O^T += V^T p   V^T as A (the codes interleaved in registers) and p as B
 //                  (movmatrix turns the accumulator layout of S^T into it).
-// Operands: codes are exact in fp16 and in int8, and no query or weight is
-// rounded to fewer bits than the result keeps.
+// Operands: codes are exact in fp16 and in int8, queries and weights are sums of
+// parts that hold about fp32's 24 bits:
 //   int8 keys: m16n8k32 on the codes as they are; a query is 4 digits of 7 bits,
 //     one product each, off by 2^-28 of the row's largest element at most (bf16:
 //     exact down to 2^-19 of it); sums are exact integers.
 //   e4m3 keys: m16n8k16 on fp16 (on sm_100a the e4m3 form of mma.sync runs as
 //     conversions and two fp16 products, so the codes are converted once here);
 //     queries as one fp16 term after a power-of-two scaling of the row to
-//     [2^14, 2^15) (exact for bf16 down to 2^-38 of the largest), fp32 ones as
-//     two (22 bits).
+//     [2^14, 2^15) (exact for bf16 down to 2^-31 of the scaling, off by 2^-39 of
+//     it below), fp32 ones as two (2^-24 of the element, or 2^-39 again).
 //   weights: two fp16 terms, relative to a power of two near the keys' scales of V
 //     and to a reference weight (2^-24, or 2^-25 of the largest weight among keys
 //     whose scales lie within 2^10 of the key's); bf16 outputs too, since what
@@ -32,7 +32,8 @@
 //     apart are taken in several turns (far_apart).
 // Statistics, sums of weights and the running output are fp32.
 //
-// What bounds it: HBM reads of the codes.  Every warp copies its tiles with
+// What bounds it: the reads of the codes, and the instructions that a tile of 32
+// rows costs beside them.  Every warp copies its tiles with
 // 16-byte cp.async into its own ring, so there is no CTA-wide barrier in
 // the loop; page-table entries are fetched one tile ahead of the copies,
 // scales one tile behind them.
@@ -407,7 +408,9 @@ struct PgWarp {
   // scale is far below the largest are left for another turn, and each turn's
   // reference is its own largest logit.  A turn is to the running sums a tile
   // of its own, so no key is lost beside one of a larger scale, whatever their
-  // weights.  (Every tile so: 102 us in place of 97 at 16 x 32K rows.)
+  // weights.  16 x 32K rows take 98 us in the usual
+  // path (102 when every tile looked for its largest logit), 136 here with one
+  // turn a tile and 233 with two.
   template <bool CAUSAL>
   __device__ __noinline__ static void far_apart(PgWarp &w, const Query &qs, uint32_t base, uint32_t mask, int key0,
                                                 const int (*lim)[2]) {
@@ -752,18 +755,21 @@ struct PgWarp {
 // (the lengths are on the device, so the cut is too): ragged batches and
 // single long sequences load every SM alike.  A segment begins with kPgHead
 // empty steps on that line, about what starting one costs a CTA, and one of up
-// to kPgWhole steps is not cut (64 ragged sequences of up to 3000 rows: 41 us
-// with 0 head steps, 27 with 2, 30 with 8; 37 of up to 9001 rows with 4 fp32
-// query tokens each: 76, 67, 76).  A segment inside one CTA is written
+// to kPgWhole steps is not cut (64 ragged sequences of up to 3000 rows: 42 us
+// with 0 head steps, 28 with 2, 31 with 8; 37 of up to 9001 rows with 4 fp32
+// query tokens each: 67, 55, 62).  A segment inside one CTA is written
 // directly; of one that several CTAs share each leaves a partial record, which
 // k_paged_join adds up in CTA order.  (Joining by the last CTA to arrive took
 // 10 us of 108 at 4 x 128K rows: 28 records of a segment, one dependent load
 // of a CTA's 4 warps behind the other.)  CTAs of 4 warps, 3 or 4 on an SM: one
 // joins its warps while the others stream.
-// Bound by the cache's bytes: 16 x 32K rows of e4m3 take 97 us (5.6 TB/s) and
-// 4 x 128K of int8 107 us (5.0 TB/s, the join of 28 records a segment in it).
-// 16 fp32 query rows are bound by matrix and issue slots: the 37 sequences
-// above, 67 us for 18 us of bytes.
+// Measured, replayed from a graph / as calls one behind the other, where the
+// power cap lowers the clock: 16 x 32K rows of e4m3 98 / 109 us (5.5 / 5.0
+// TB/s), 4 x 128K of int8 111 / 121 us (4.8 / 4.4 TB/s); DRAM is busy 58 and 50
+// % of the kernel, issue slots 55 and 41 %, and most waits are for fixed
+// latencies.  16 fp32 query rows (the 37 sequences above): 55 us for 18 us of
+// bytes, tensor pipe 30 % and issue slots 44 % busy, 12 warps an SM too few to
+// cover the rest.
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgStep = 32 * kPgWarps;  // rows of one CTA step
@@ -856,8 +862,8 @@ __device__ __forceinline__ int paged_find(const uint32_t *pre, int B, uint32_t p
   return lo;
 }
 
-// Dynamic shared memory: rings (over them, once drained, the warps' results
-// and the weights of a join) | queries | prefix sums [B + 1] and lengths [B].
+// Dynamic shared memory: rings (over them, once drained, the warps' results) |
+// queries | prefix sums [B + 1] and lengths [B].
 template <int D, int FMT, bool QF32, int NT>
 __host__ __device__ constexpr uint32_t paged_attend_smem() {
   return kPgWarps * PgCfg<D>::kRing + sizeof(PgQuery<D, FMT, QF32, NT>);
@@ -869,7 +875,6 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D>::kCtas) k_paged_attend(co
   using Query = typename Warp::Query;
   constexpr int R = 8 * NT, kRec = D + kPartHeader;
   static_assert(PgCfg<D>::kRing >= R * kRec * 4, "the warps' results fit over the rings");
-  static_assert(kPgWarps * PgCfg<D>::kRing >= 8 * kPgMaxCtas * 4, "the weights of a join fit over the rings");
   extern __shared__ __align__(128) uint8_t smem[];
   Query &qs = *reinterpret_cast<Query *>(smem + kPgWarps * PgCfg<D>::kRing);
   uint32_t *pre = reinterpret_cast<uint32_t *>(smem + paged_attend_smem<D, FMT, QF32, NT>());
@@ -1093,8 +1098,8 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedAttendArgs a) {
 // span chunks and pages); one of the 8 query columns is in use.  The gists
 // of selected chunks (exclude mode) are summed on the CUDA cores while the
 // first copies are in flight, as a record of their own.  A CTA streams too
-// little to hide its start and end: top-64 of 16 x 32K rows takes 14.1 us for
-// 5.9 us of bytes, top-128 of 4 x 128K 23.9 for 9.6, 2 x 512K 15.6 for 5.3
+// little to hide its start and end: top-64 of 16 x 32K rows takes 15.8 us for
+// 5.9 us of bytes, top-128 of 4 x 128K 26.7 for 9.6, 2 x 512K 17.3 for 5.3
 // (neighbouring chunks in place of random ones: the same time).
 struct PagedUnfoldArgs {
   UnfoldArgs u;  // raw_k, raw_v and the tensor maps unused
