@@ -408,9 +408,9 @@ struct PgWarp {
   // scale is far below the largest are left for another turn, and each turn's
   // reference is its own largest logit.  A turn is to the running sums a tile
   // of its own, so no key is lost beside one of a larger scale, whatever their
-  // weights.  16 x 32K rows take 98 us in the usual
-  // path (102 when every tile looked for its largest logit), 136 here with one
-  // turn a tile and 233 with two.
+  // weights.  16 x 32K rows take 98 us in the usual path (102 when every tile
+  // looked for its largest logit), 136 here with one turn a tile and 233 with
+  // two.
   template <bool CAUSAL>
   __device__ __noinline__ static void far_apart(PgWarp &w, const Query &qs, uint32_t base, uint32_t mask, int key0,
                                                 const int (*lim)[2]) {
@@ -764,8 +764,8 @@ struct PgWarp {
 // of a CTA's 4 warps behind the other.)  CTAs of 4 warps, 3 or 4 on an SM: one
 // joins its warps while the others stream.
 // Measured, replayed from a graph / as calls one behind the other, where the
-// power cap lowers the clock: 16 x 32K rows of e4m3 98 / 109 us (5.5 / 5.0
-// TB/s), 4 x 128K of int8 111 / 121 us (4.8 / 4.4 TB/s); DRAM is busy 58 and 50
+// power cap lowers the clock: 16 x 32K rows of e4m3 98 / 109 to 117 us (5.5 /
+// 5.0 TB/s), 4 x 128K of int8 111 / 121 to 129 (4.8 / 4.4); DRAM is busy 58 and 50
 // % of the kernel, issue slots 55 and 41 %, and most waits are for fixed
 // latencies.  16 fp32 query rows (the 37 sequences above): 55 us for 18 us of
 // bytes, tensor pipe 30 % and issue slots 44 % busy, 12 warps an SM too few to
